@@ -18,6 +18,8 @@ LIB_PATH = os.environ.get("MOEFFN_LIB") or os.path.join(HERE, "libmoeffn.so")
 MOE_F16, MOE_BF16, MOE_F32 = 0, 1, 2
 PATH_SPARSE, PATH_DENSE, PATH_AUTO, PATH_MIXED = 0, 1, 2, 3
 OP_EXPERT, OP_ROUTE, OP_LAYER, OP_CALIBRATE, OP_EAMC, OP_EXPERT_BITS = 0, 1, 2, 3, 4, 5
+OP_LINEAR, OP_LAYER_FEW = 6, 7
+ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
           -3: "MOE_ERR_ALIGNMENT", -4: "MOE_ERR_WORKSPACE", -5: "MOE_ERR_HIP"}
@@ -28,7 +30,8 @@ EXPORTED = ["moe_route_topk", "moe_expert_forward_sparse", "moe_layer_forward",
             "moe_eamc_match", "moe_expert_forward_sparse_bits", "moe_pack_up_bits",
             "moe_build_sources_sha256", "moe_expert_forward_sparse_noalloc",
             "moe_noalloc_scratch_bytes", "moe_materialize_up", "moe_transpose_down",
-            "moe_auto_dense_min", "moe_mixed_dense_min"]
+            "moe_auto_dense_min", "moe_mixed_dense_min", "moe_layer_forward_few",
+            "moe_linear_forward"]
 
 
 class MoeError(RuntimeError):
@@ -55,6 +58,12 @@ class LayerTrace(C.Structure):
     _fields_ = [("topk_idx", C.c_void_p), ("topk_w", C.c_void_p), ("logits", C.c_void_p),
                 ("expert_count", C.c_void_p), ("masks", C.c_void_p), ("eam_row", C.c_void_p),
                 ("mask_bits", C.c_void_p), ("nnz", C.c_void_p), ("expert_dense", C.c_void_p)]
+
+
+class LinearDesc(C.Structure):
+    _fields_ = [("n", C.c_int), ("k", C.c_int), ("wdt", C.c_int), ("w", C.c_void_p),
+                ("bias", C.c_void_p), ("w_gate", C.c_void_p), ("bias_gate", C.c_void_p),
+                ("act", C.c_int)]
 
 
 _lib = None
@@ -117,6 +126,12 @@ def lib():
         L.moe_pack_up_bits.argtypes = [P, I, I, I, I, P, P, P]
         L.moe_eamc_match.restype = I
         L.moe_eamc_match.argtypes = [P, I, I, P, P, P, P, Z, P]
+        L.moe_layer_forward_few.restype = I
+        L.moe_layer_forward_few.argtypes = [C.POINTER(LayerDesc), P, I, I, P, P, I,
+                                            C.POINTER(LayerTrace), P, Z, P]
+        L.moe_linear_forward.restype = I
+        L.moe_linear_forward.argtypes = [C.POINTER(LinearDesc), P, I, C.c_longlong, I, P,
+                                         C.c_longlong, P, I, C.c_longlong, P, Z, P]
         _lib = L
     return _lib
 
@@ -335,6 +350,152 @@ def layer_forward(layer: Layer, x, *, path: int = PATH_SPARSE, y=None, out_dtype
                                  C.byref(tr) if tr is not None else None, _ptr(ws), ws.numel(),
                                  _stream())
     _check(st, "moe_layer_forward")
+    return y
+
+
+def _on(x, **others):
+    """Checks that the tensors of a call lie on x's GPU (None allowed)."""
+    if x.device.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    for name, t in others.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+
+
+def _shaped(name, t, shape, dtype=None):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
+def _rows(name, t, align=1):
+    """(data pointer, row stride) of a matrix whose rows are contiguous.  The
+    stride of a single row means nothing and is taken as the row's length."""
+    if t is None:
+        return None, 0
+    n = t.shape[1]
+    if t.stride(1) != 1 and n > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    stride = t.stride(0) if t.shape[0] > 1 else (n + align - 1) // align * align
+    return t.data_ptr(), stride
+
+
+_TRACE_DTYPES = {"topk_idx": "int32", "topk_w": "float32", "logits": "float32", "expert_count": "int32",
+                 "eam_row": "int32", "expert_dense": "uint8"}
+
+
+def layer_forward_few(layer: Layer, x, *, residual=None, y=None, out_dtype=None,
+                      trace: Optional[dict] = None, ws=None):
+    """One layer of plain 16-bit experts on the few tokens (1 to 32) of a decode
+    step, x [T][d]; returns y [T][d] = residual + the layer's output.
+
+    Reads the layer's router, gate_t, up_dense and down_dense; its up_q, up_sz,
+    down and thresholds may be None.  ``residual`` [T][d] has y's type and may be
+    y.  ``trace`` maps any of topk_idx [T][k], topk_w [T][k], logits [T][E],
+    expert_count [E], expert_dense [E] and eam_row [E] to device tensors as in
+    layer_forward."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [T][d]")
+    T, d = x.shape
+    E, S, f, k = layer.E, layer.S, layer.f, layer.k
+    trace = trace or {}
+    _on(x, residual=residual, y=y, ws=ws, router_w=layer.router_w, router_bias=layer.router_bias,
+        gate_t=layer.gate_t, up_dense=layer.up_dense, down_dense=layer.down_dense, **trace)
+    _shaped("x", x, (T, layer.d))
+    if layer.up_dense is None or layer.down_dense is None:
+        raise ValueError("the layer needs up_dense and down_dense")
+    _shaped("router_w", layer.router_w, (E, d))
+    if layer.router_bias is not None:
+        _shaped("router_bias", layer.router_bias, (E,), torch.float32)
+    _shaped("gate_t", layer.gate_t, (E + S, f, d))
+    _shaped("up_dense", layer.up_dense, (E + S, f, d), layer.gate_t.dtype)
+    _shaped("down_dense", layer.down_dense, (E + S, d, f), layer.gate_t.dtype)
+    if y is None:
+        y = torch.empty((T, d), dtype=out_dtype or torch.float32, device=x.device)
+    _shaped("y", y, (T, d))
+    if residual is not None:
+        _shaped("residual", residual, (T, d), y.dtype)
+    shapes = {"topk_idx": (T, k), "topk_w": (T, k), "logits": (T, E)}
+    for name, t in trace.items():
+        if t is None:
+            continue
+        if name not in _TRACE_DTYPES:
+            raise ValueError(f"layer_forward_few exports no {name}")
+        _shaped(name, t, shapes.get(name, (E,)), getattr(torch, _TRACE_DTYPES[name]))
+    with torch.cuda.device(x.device):
+        if ws is None:
+            ws = torch.empty(max(256, workspace_size(OP_LAYER_FEW, T, d, f, E, k, S)),
+                             dtype=torch.uint8, device=x.device)
+        tr = LayerTrace(**{name: _ptr(t) for name, t in trace.items()}) if trace else None
+        desc = layer.desc()
+        st = lib().moe_layer_forward_few(C.byref(desc), _ptr(x), _dt(x), T, _ptr(residual), _ptr(y),
+                                         _dt(y), C.byref(tr) if tr is not None else None, _ptr(ws),
+                                         ws.numel() * ws.element_size(), _stream())
+    _check(st, "moe_layer_forward_few")
+    return y
+
+
+@dataclass
+class Linear:
+    """A linear layer, y = act(x W^T + bias), or with w_gate
+    y = act(x w_gate^T + bias_gate) * (x W^T + bias)."""
+    w: "torch.Tensor"                           # [n][k] fp16/bf16
+    bias: Optional["torch.Tensor"] = None       # [n] fp32
+    w_gate: Optional["torch.Tensor"] = None     # [n][k]
+    bias_gate: Optional["torch.Tensor"] = None  # [n] fp32
+    act: str = "none"                           # a key of ACT
+
+    @property
+    def n(self):
+        return self.w.shape[0]
+
+    @property
+    def k(self):
+        return self.w.shape[1]
+
+    def desc(self) -> LinearDesc:
+        if self.act not in ACT:
+            raise ValueError(f"act must be one of {sorted(ACT)}")
+        return LinearDesc(self.n, self.k, _dt(self.w), _ptr(self.w), _ptr(self.bias),
+                          _ptr(self.w_gate), _ptr(self.bias_gate), ACT[self.act])
+
+
+def linear_forward(linear: Linear, x, *, residual=None, y=None, out_dtype=None, ws=None):
+    """residual + the linear layer on x [T][k]; returns y [T][n].
+
+    x, y and residual may be row-strided (contiguous rows; x's row stride a
+    multiple of 8).  ``residual`` has y's type and may be y."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [T][k]")
+    T, (n, k) = x.shape[0], linear.w.shape
+    _on(x, residual=residual, y=y, ws=ws, w=linear.w, bias=linear.bias, w_gate=linear.w_gate,
+        bias_gate=linear.bias_gate)
+    _shaped("x", x, (T, k))
+    for name in ("bias", "bias_gate"):
+        t = getattr(linear, name)
+        if t is not None:
+            _shaped(name, t, (n,), torch.float32)
+    if linear.w_gate is not None:
+        _shaped("w_gate", linear.w_gate, (n, k), linear.w.dtype)
+    if y is None:
+        y = torch.empty((T, n), dtype=out_dtype or torch.float32, device=x.device)
+    _shaped("y", y, (T, n))
+    if residual is not None:
+        _shaped("residual", residual, (T, n), y.dtype)
+    xp, xs = _rows("x", x, 8)
+    yp, ys = _rows("y", y)
+    rp, rs = _rows("residual", residual)
+    with torch.cuda.device(x.device):
+        if ws is None:
+            ws = torch.empty(max(256, workspace_size(OP_LINEAR, T, k, n)), dtype=torch.uint8,
+                             device=x.device)
+        desc = linear.desc()
+        st = lib().moe_linear_forward(C.byref(desc), xp, _dt(x), xs, T, rp, rs, yp, _dt(y), ys,
+                                      _ptr(ws), ws.numel() * ws.element_size(), _stream())
+    _check(st, "moe_linear_forward")
     return y
 
 

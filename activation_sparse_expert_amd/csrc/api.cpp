@@ -9,6 +9,7 @@
 
 #include "../../include/moeffn.h"
 #include "internal.hpp"
+#include "linear.hpp"
 
 using namespace moeffn;
 
@@ -422,6 +423,58 @@ bool auto_dense(const moe_layer *L, int T)
     return layer_old_ok(L) && (long long)T * L->top_k >= 8ll * L->n_routed;
 }
 
+constexpr int kLinearMaxT = 65536, kLinearMaxK = 1 << 20, kLinearMaxN = 1 << 24;
+
+bool linear_size_ok(int T, int k, int n)
+{
+    return T >= 1 && T <= kLinearMaxT && k >= 8 && k % 8 == 0 && k <= kLinearMaxK && n >= 1 && n <= kLinearMaxN;
+}
+
+size_t linear_ws_bytes(int T, int k, int n)
+{
+    return T <= kStreamTokens ? kAlign : up(linear_tile_ws_bytes(T, k, n)) + kAlign;
+}
+
+bool few_size_ok(int T, int d, int f, int E, int k, int S)
+{
+    return T >= 1 && T <= kFewTokens && d >= 8 && d % 8 == 0 && d <= 16384 && f >= 8 && f % 8 == 0 && E >= 1 &&
+           E <= 1024 && k >= 1 && k <= E && S >= 0 && (long long)T * (k + (long long)S) <= kFewRows;
+}
+
+struct FewWs {
+    int32_t *topk_idx;
+    float *topk_w, *lg;
+    FewTab tab;
+    uint16_t *h;
+};
+
+int few_amax(int T, int E, int k, int S) { return (E < T * k ? E : T * k) + S; }
+
+size_t few_ws_bytes(int T, int f, int E, int k, int S, FewWs *out, void *base)
+{
+    const size_t rows = (size_t)T * (k + S), amax = few_amax(T, E, k, S);
+    const size_t size[9] = {(size_t)T * k * 4, (size_t)T * k * 4, (size_t)T * E * 4, 4,
+                            amax * 4, amax * 4, amax * 4, rows * 4, rows * f * 4};
+    size_t off[9], o = 0;
+    for (int i = 0; i < 9; ++i) {
+        off[i] = o;
+        o += up(size[i]);
+    }
+    if (out) {
+        char *p = (char *)base;
+        out->topk_idx = (int32_t *)(p + off[0]);
+        out->topk_w = (float *)(p + off[1]);
+        out->lg = (float *)(p + off[2]);
+        out->tab.n = (int32_t *)(p + off[3]);
+        out->tab.expert = (int32_t *)(p + off[4]);
+        out->tab.mask = (uint32_t *)(p + off[5]);
+        out->tab.off = (int32_t *)(p + off[6]);
+        out->tab.wt = (float *)(p + off[7]);
+        out->h = (uint16_t *)(p + off[8]);
+    }
+    return o;
+}
+
 // MOE_PATH_MIXED for T tokens: the per-expert token threshold, or 0 when no
 // expert can reach it (or the layer has no GEMM weights)
 int mixed_dense_min(const moe_layer *L, int T)
@@ -472,6 +525,10 @@ size_t moe_workspace_size(moe_op op, int T, int d, int f, int E, int k, int S)
         return f < 1 ? 0 : expert_ws_bytes(T, d, f);
     case MOE_OP_EAMC:
         return d > kEamcMaxLen ? 0 : up((size_t)T * 8);   // T stored EAMs of d entries
+    case MOE_OP_LINEAR:
+        return linear_size_ok(T, d, f) ? linear_ws_bytes(T, d, f) : 0;
+    case MOE_OP_LAYER_FEW:
+        return few_size_ok(T, d, f, E, k, S) ? few_ws_bytes(T, f, E, k, S, nullptr, nullptr) : 0;
     }
     return 0;
 }
@@ -892,6 +949,95 @@ moe_status moe_layer_forward(const moe_layer *L, const void *x, moe_dtype xdt, i
     if (he == hipSuccess && want_bits)
         he = launch_mask_bits(a.mask_out, T * (k + S), f, trace->mask_bits, trace->nnz, s);
     return hip_status(he);
+}
+
+moe_status moe_layer_forward_few(const moe_layer *L, const void *x, moe_dtype xdt, int T,
+                                 const void *residual, void *y, moe_dtype ydt,
+                                 const moe_layer_trace *trace, void *ws, size_t ws_bytes,
+                                 void *stream)
+{
+    if (!L || !x || !y) return MOE_ERR_INVALID_ARG;
+    const int d = L->d, f = L->f, E = L->n_routed, S = L->n_shared, k = L->top_k;
+    if (S < 0 || f < 1) return MOE_ERR_INVALID_ARG;
+    moe_status st = check_route_args(x, xdt, T, d, L->router_w, L->rdt, E, k);
+    if (st != MOE_OK) return st;
+    if (!L->gate_t || !L->up_dense || !L->down_dense) return MOE_ERR_INVALID_ARG;
+    if (!few_size_ok(T, d, f, E, k, S)) return MOE_ERR_UNSUPPORTED;
+    if (!is16(L->wdt) || xdt != L->wdt || !valid_out(ydt)) return MOE_ERR_UNSUPPORTED;
+    const size_t ya = ydt == MOE_F32 ? 4 : 2;
+    if (!aligned(x, 16) || !aligned(y, ya) || !aligned(residual, ya) || !aligned(L->gate_t, 16) ||
+        !aligned(L->up_dense, 16) || !aligned(L->down_dense, 16) || !aligned(L->router_w, 16) ||
+        !aligned(L->router_bias, 4))
+        return MOE_ERR_ALIGNMENT;
+    if (trace) {
+        if (trace->masks || trace->mask_bits || trace->nnz) return MOE_ERR_UNSUPPORTED;
+        if (!aligned(trace->topk_idx, 4) || !aligned(trace->topk_w, 4) || !aligned(trace->logits, 4) ||
+            !aligned(trace->expert_count, 4) || !aligned(trace->eam_row, 4))
+            return MOE_ERR_ALIGNMENT;
+    }
+    if (!ws || ws_bytes < few_ws_bytes(T, f, E, k, S, nullptr, nullptr)) return MOE_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return MOE_ERR_ALIGNMENT;
+
+    hipStream_t s = (hipStream_t)stream;
+    FewWs w;
+    few_ws_bytes(T, f, E, k, S, &w, ws);
+    RouteArgs r{};
+    r.x = x; r.xdt = xdt; r.T = T; r.d = d;
+    r.rw = L->router_w; r.rdt = L->rdt; r.bias = L->router_bias;
+    r.E = E; r.k = k; r.renorm = L->renormalize ? 1 : 0;
+    r.topk_idx = (trace && trace->topk_idx) ? trace->topk_idx : w.topk_idx;
+    r.topk_w = (trace && trace->topk_w) ? trace->topk_w : w.topk_w;
+    r.logits = trace ? trace->logits : nullptr;
+    r.lg_buf = route_split(d, E, L->rdt) ? w.lg : nullptr;
+    hipError_t he = launch_route(r, s);
+    if (he != hipSuccess) return MOE_ERR_HIP;
+    FewArgs a{};
+    a.T = T; a.d = d; a.f = f; a.E = E; a.k = k; a.S = S;
+    a.bf16 = L->wdt == MOE_BF16 ? 1 : 0; a.ydt = (int)ydt;
+    a.x = (const uint16_t *)x;
+    a.gate = (const uint16_t *)L->gate_t; a.up = L->up_dense; a.down_t = (const uint16_t *)L->down_dense;
+    a.topk_idx = r.topk_idx; a.topk_w = r.topk_w;
+    a.tab = w.tab; a.amax = few_amax(T, E, k, S); a.h = w.h;
+    a.r = residual; a.y = y;
+    if (trace) {
+        a.count = trace->expert_count; a.eam_row = trace->eam_row; a.expert_dense = trace->expert_dense;
+    }
+    he = launch_few_gateup(a, s);
+    if (he == hipSuccess) he = launch_few_down(a, s);
+    return hip_status(he);
+}
+
+moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt, long long x_stride,
+                              int T, const void *residual, long long residual_stride, void *y,
+                              moe_dtype ydt, long long y_stride, void *ws, size_t ws_bytes,
+                              void *stream)
+{
+    if (!L || !x || !y || !L->w) return MOE_ERR_INVALID_ARG;
+    const int n = L->n, k = L->k;
+    if (T < 1 || T > kLinearMaxT || n < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+    if (L->act < MOE_ACT_NONE || L->act > MOE_ACT_SILU || (L->bias_gate && !L->w_gate)) return MOE_ERR_INVALID_ARG;
+    if (x_stride < k || y_stride < n || (residual && residual_stride < n)) return MOE_ERR_INVALID_ARG;
+    if (residual == y && residual_stride != y_stride) return MOE_ERR_INVALID_ARG;
+    if (!linear_size_ok(T, k, n)) return MOE_ERR_UNSUPPORTED;
+    if (!is16(L->wdt) || xdt != L->wdt || !valid_out(ydt)) return MOE_ERR_UNSUPPORTED;
+    const size_t ya = ydt == MOE_F32 ? 4 : 2;
+    if (!aligned(x, 16) || x_stride % 8 != 0 || !aligned(L->w, 16) || !aligned(L->w_gate, 16) || !aligned(y, ya) ||
+        !aligned(residual, ya) || !aligned(L->bias, 4) || !aligned(L->bias_gate, 4))
+        return MOE_ERR_ALIGNMENT;
+    if (!ws || ws_bytes < linear_ws_bytes(T, k, n)) return MOE_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return MOE_ERR_ALIGNMENT;
+    LinearArgs a{};
+    a.T = T; a.K = k; a.N = n;
+    a.bf16 = L->wdt == MOE_BF16 ? 1 : 0;
+    a.act = (int)L->act; a.ydt = (int)ydt;
+    a.x = (const uint16_t *)x; a.xs = x_stride;
+    a.w = (const uint16_t *)L->w; a.wg = (const uint16_t *)L->w_gate;
+    a.b = L->bias; a.bg = L->bias_gate;
+    a.r = residual; a.rs = residual_stride;
+    a.y = y; a.ys = y_stride;
+    a.part = (float *)ws;
+    hipStream_t s = (hipStream_t)stream;
+    return hip_status(T <= kStreamTokens ? launch_linear_stream(a, s) : launch_linear_tile(a, s));
 }
 
 moe_status moe_pack_up_int2(const void *w_up_t, moe_dtype dt, int d, int f, uint8_t *up_q,

@@ -105,8 +105,18 @@ typedef MOE_ENUM {
     MOE_OP_LAYER = 2,           /* moe_layer_forward        */
     MOE_OP_CALIBRATE = 3,       /* moe_calibrate_threshold  */
     MOE_OP_EAMC = 4,            /* moe_eamc_match (T = n, d = len) */
-    MOE_OP_EXPERT_BITS = 5      /* moe_expert_forward_sparse_bits, any width */
+    MOE_OP_EXPERT_BITS = 5,     /* moe_expert_forward_sparse_bits, any width */
+    MOE_OP_LINEAR = 6,          /* moe_linear_forward (d = inputs, f = outputs) */
+    MOE_OP_LAYER_FEW = 7        /* moe_layer_forward_few    */
 } moe_op;
+
+typedef MOE_ENUM {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,
+    MOE_ACT_GELU = 2,           /* v (1 + erf(v / sqrt 2)) / 2 */
+    MOE_ACT_GELU_TANH = 3,      /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+    MOE_ACT_SILU = 4            /* v / (1 + exp(-v)) */
+} moe_act;
 
 /* One compressed expert (FloE review, "混合压缩策略": {W^S(gate), W^S(down),
  * W^Q(up)}; Algorithm 1 inputs E_ij and t_ij). */
@@ -149,6 +159,17 @@ typedef struct {
                                    sparsity); <= 0: 0.5.  Read by MOE_PATH_AUTO
                                    and MOE_PATH_MIXED only.                  */
 } moe_layer;
+
+/* One linear layer, plain or gated (moe_linear_forward). */
+typedef struct {
+    int n, k;                   /* outputs, inputs                         */
+    moe_dtype wdt;              /* weight (and activation) type: f16 or bf16 */
+    const void *w;              /* [n][k], row j = column j of W           */
+    const float *bias;          /* [n] or NULL                             */
+    const void *w_gate;         /* [n][k], row j = column j of W^gate; NULL: not gated */
+    const float *bias_gate;     /* [n] or NULL (gated layers only)         */
+    moe_act act;                /* of the product, or of the gate's when gated */
+} moe_linear;
 
 /* Optional device outputs of moe_layer_forward (any field may be NULL). */
 typedef struct {
@@ -310,6 +331,52 @@ moe_status moe_layer_forward(const moe_layer *L, const void *x, moe_dtype xdt, i
                              void *y, moe_dtype ydt, moe_path path,
                              const moe_layer_trace *trace,
                              void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The same layer on plain 16-bit experts for the few tokens of a decode step
+ * (T from 1 to 32), with the caller's residual added:
+ *   y_t = residual_t + sum_s w_{t,s} a_{e(t,s)}(x_t) + sum_i a_{E+i}(x_t),
+ *   a_e(x) = (SiLU(x W^gate) (.) x W^up) W^down
+ * (FloE review, "MoE 专家前向计算"; routing as moe_route_topk).  The weights of
+ * the experts that some token chose are read once, whatever the tokens.
+ * Of L it reads d, f (both multiples of 8), n_routed, n_shared, top_k,
+ * renormalize, wdt, the router, gate_t, up_dense and down_dense, which all have
+ * to be there; the INT2 codes, `down` and the thresholds are not read and may be
+ * NULL.  Weights with infinities or NaN touch only the tokens sent to them.
+ *   x [T][d] in xdt (== L->wdt), y [T][d] in ydt, residual [T][d] in ydt or
+ *   NULL; residual and x may be y itself.  SiLU(g) u is kept to about 17 bits
+ *   (bf16 layers) or 22 (fp16 layers, infinite beyond 65504), all sums in fp32.
+ *   Bit-reproducible for the same call; the order of a token's sums may depend
+ *   on which experts the call's other tokens chose.
+ * trace as moe_layer_forward's for the dense path (no masks, bits or nnz).
+ * Limits: T (k + S) <= 2048, E <= 1024 (else MOE_ERR_UNSUPPORTED).
+ * Workspace: moe_workspace_size(MOE_OP_LAYER_FEW, T, d, f, E, k, S) bytes.
+ */
+moe_status moe_layer_forward_few(const moe_layer *L, const void *x, moe_dtype xdt, int T,
+                                 const void *residual, void *y, moe_dtype ydt,
+                                 const moe_layer_trace *trace,
+                                 void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * A linear layer with its bias, activation, gate and residual in the epilogue
+ * of the product (the dense FFN layers and projections around the MoE layers):
+ *   y = residual + act(x W^T + bias), or with L->w_gate
+ *   y = residual + act(x Wg^T + bias_gate) (.) (x W^T + bias)
+ * with fp32 sums and one rounding, to ydt.
+ *   x [T][k] in xdt (== L->wdt), y [T][n] in ydt, residual [T][n] in ydt or
+ *   NULL; rows at x_stride, y_stride and residual_stride elements (at least the
+ *   row's length; x_stride a multiple of 8).  residual may be y itself, at
+ *   the same stride; y must not overlap x or the weights otherwise.
+ * Limits: 1 <= T <= 65536; k a multiple of 8 up to 2^20, n up to 2^24 (else
+ * MOE_ERR_UNSUPPORTED); x and the weights 16-byte aligned.  The order of the
+ * sums depends on T, n and k alone: outputs are bit-reproducible.
+ * Workspace: moe_workspace_size(MOE_OP_LINEAR, T, k, n, 0, 0, 0) bytes, gated or
+ * not.
+ */
+moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt, long long x_stride,
+                              int T, const void *residual, long long residual_stride,
+                              void *y, moe_dtype ydt, long long y_stride,
+                              void *ws, size_t ws_bytes, void *stream);
 
 /*
  * MOE_PATH_AUTO's choice for a call of T tokens on this layer (without mask
