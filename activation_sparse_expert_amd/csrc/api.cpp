@@ -442,8 +442,7 @@ bool few_size_ok(int T, int d, int f, int E, int k, int S)
 }
 
 struct FewWs {
-    int32_t *topk_idx;
-    float *topk_w, *lg;
+    float *lg;
     FewTab tab;
     uint16_t *h;
 };
@@ -453,24 +452,21 @@ int few_amax(int T, int E, int k, int S) { return (E < T * k ? E : T * k) + S; }
 size_t few_ws_bytes(int T, int f, int E, int k, int S, FewWs *out, void *base)
 {
     const size_t rows = (size_t)T * (k + S), amax = few_amax(T, E, k, S);
-    const size_t size[9] = {(size_t)T * k * 4, (size_t)T * k * 4, (size_t)T * E * 4, 4,
-                            amax * 4, amax * 4, amax * 4, rows * 4, rows * f * 4};
-    size_t off[9], o = 0;
-    for (int i = 0; i < 9; ++i) {
+    const size_t size[7] = {(size_t)T * E * 4, 4, amax * 4, (amax + 1) * 4, rows * 4, rows * 4, rows * f * 4};
+    size_t off[7], o = 0;
+    for (int i = 0; i < 7; ++i) {
         off[i] = o;
         o += up(size[i]);
     }
     if (out) {
         char *p = (char *)base;
-        out->topk_idx = (int32_t *)(p + off[0]);
-        out->topk_w = (float *)(p + off[1]);
-        out->lg = (float *)(p + off[2]);
-        out->tab.n = (int32_t *)(p + off[3]);
-        out->tab.expert = (int32_t *)(p + off[4]);
-        out->tab.mask = (uint32_t *)(p + off[5]);
-        out->tab.off = (int32_t *)(p + off[6]);
-        out->tab.wt = (float *)(p + off[7]);
-        out->h = (uint16_t *)(p + off[8]);
+        out->lg = (float *)(p + off[0]);
+        out->tab.n = (int32_t *)(p + off[1]);
+        out->tab.expert = (int32_t *)(p + off[2]);
+        out->tab.off = (int32_t *)(p + off[3]);
+        out->tab.tok = (int32_t *)(p + off[4]);
+        out->tab.wt = (float *)(p + off[5]);
+        out->h = (uint16_t *)(p + off[6]);
     }
     return o;
 }
@@ -984,25 +980,24 @@ moe_status moe_layer_forward_few(const moe_layer *L, const void *x, moe_dtype xd
     RouteArgs r{};
     r.x = x; r.xdt = xdt; r.T = T; r.d = d;
     r.rw = L->router_w; r.rdt = L->rdt; r.bias = L->router_bias;
-    r.E = E; r.k = k; r.renorm = L->renormalize ? 1 : 0;
-    r.topk_idx = (trace && trace->topk_idx) ? trace->topk_idx : w.topk_idx;
-    r.topk_w = (trace && trace->topk_w) ? trace->topk_w : w.topk_w;
-    r.logits = trace ? trace->logits : nullptr;
-    r.lg_buf = route_split(d, E, L->rdt) ? w.lg : nullptr;
-    hipError_t he = launch_route(r, s);
+    r.E = E;
+    r.lg_buf = w.lg;
+    hipError_t he = launch_route_logits(r, s);
     if (he != hipSuccess) return MOE_ERR_HIP;
     FewArgs a{};
     a.T = T; a.d = d; a.f = f; a.E = E; a.k = k; a.S = S;
     a.bf16 = L->wdt == MOE_BF16 ? 1 : 0; a.ydt = (int)ydt;
     a.x = (const uint16_t *)x;
     a.gate = (const uint16_t *)L->gate_t; a.up = L->up_dense; a.down_t = (const uint16_t *)L->down_dense;
-    a.topk_idx = r.topk_idx; a.topk_w = r.topk_w;
+    a.lg = w.lg; a.renorm = L->renormalize ? 1 : 0;
     a.tab = w.tab; a.amax = few_amax(T, E, k, S); a.h = w.h;
     a.r = residual; a.y = y;
     if (trace) {
+        a.topk_idx = trace->topk_idx; a.topk_w = trace->topk_w; a.logits = trace->logits;
         a.count = trace->expert_count; a.eam_row = trace->eam_row; a.expert_dense = trace->expert_dense;
     }
-    he = launch_few_gateup(a, s);
+    he = launch_few_rank(a, s);
+    if (he == hipSuccess) he = launch_few_gateup(a, s);
     if (he == hipSuccess) he = launch_few_down(a, s);
     return hip_status(he);
 }

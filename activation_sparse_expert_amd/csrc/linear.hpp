@@ -30,16 +30,15 @@ hipError_t launch_linear_stream(const LinearArgs &a, hipStream_t s);    // T <= 
 hipError_t launch_linear_tile(const LinearArgs &a, hipStream_t s);      // any T
 size_t linear_tile_ws_bytes(int T, int K, int N);       // the larger of the plain and the gated call's
 
-// The few-token MoE layer: the call's experts and their tokens, made by every
-// gate/up workgroup from the routing, and kept for the down product by one.
-// Experts with tokens are listed in ascending order, the shared ones last; a
-// token's place in expert a is row off[a] + (set bits of mask[a] below it).
+// The few-token MoE layer: the experts of a call and their tokens, made from the
+// routing once.  Experts with tokens are listed in ascending order, the shared ones
+// last; expert i's tokens are rows off[i] .. off[i + 1] - 1, ascending.
 struct FewTab {
     int32_t *n;                         // [1] experts listed
     int32_t *expert;                    // [A]
-    uint32_t *mask;                     // [A] bit t: token t goes to the expert
-    int32_t *off;                       // [A] first row
-    float *wt;                          // [T (k + S)] router weight of each row
+    int32_t *off;                       // [A + 1]
+    int32_t *tok;                       // [T (k + S)] token of each row
+    float *wt;                          // [T (k + S)] its router weight (shared experts: 1)
 };
 
 struct FewArgs {
@@ -48,19 +47,22 @@ struct FewArgs {
     const uint16_t *x;                  // [T][d]
     const uint16_t *gate, *up;          // [E+S][f][d]
     const uint16_t *down_t;             // [E+S][d][f]
-    const int32_t *topk_idx;            // [T][k]
-    const float *topk_w;                // [T][k]
+    const float *lg;                    // [T][E] router logits
+    int renorm;
     FewTab tab;
     int amax;                           // bound of the listed experts: min(E, T k) + S
-    uint16_t *h;                        // [T (k + S)][f / 8][8 hi, 8 lo] (workspace)
+    uint16_t *h;                        // [T (k + S)][hi, lo][f] (workspace)
     const void *r;                      // [T][d] or null
     void *y;                            // [T][d]
-    int32_t *count, *eam_row;           // trace exports or null
+    int32_t *topk_idx;                  // trace exports or null
+    float *topk_w, *logits;
+    int32_t *count, *eam_row;
     uint8_t *expert_dense;
 };
 
-constexpr int kFewTokens = 32;          // bits of a token mask
+constexpr int kFewTokens = 32;
 constexpr int kFewRows = 2048;          // T (k + S)
+hipError_t launch_few_rank(const FewArgs &a, hipStream_t s);
 hipError_t launch_few_gateup(const FewArgs &a, hipStream_t s);
 hipError_t launch_few_down(const FewArgs &a, hipStream_t s);
 

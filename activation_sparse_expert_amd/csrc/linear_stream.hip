@@ -1,8 +1,9 @@
-// Linear layer for at most 32 tokens: the weights are read once, from HBM into
-// the matrix core's operand registers (mfma_stream.hpp).  A wave takes 16
-// outputs (of both matrices when gated) and a slice of K; the P waves of a
-// workgroup that share the outputs add their slices through LDS in a fixed
-// order and apply the epilogue.
+// Linear layer for at most 32 tokens: the weights are read once, past all tokens
+// (mfma_stream.hpp).  A wave takes 16 NM weight rows (of both matrices when
+// gated) and a slice of K; the P waves of a workgroup that share the rows add
+// their slices through LDS in a fixed order and apply the epilogue.  Workgroups
+// are small, so that several share a compute unit and one streams while
+// another starts or ends.
 #include "linear_epilogue.hpp"
 
 namespace moeffn {
@@ -11,78 +12,110 @@ namespace {
 
 using st::floatx4;
 
-// NM: matrices (2 gated); NB: groups of 16 tokens; U: steps of 32 k in flight.
-template <bool BF16, int NM, int NB, int U>
+// NM: groups of 16 weight rows per wave, the second half of Wg when GATED;
+// XI: groups of 8 tokens; D: blocks in the ring.
+template <bool BF16, bool GATED, int NM, int XI, int D>
 __global__ void __launch_bounds__(1024)
 linear_stream_kernel(LinearArgs a, int P, int slice)
 {
-    extern __shared__ __align__(16) float red[];    // [waves][NM][NB][64 lanes][4]
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int G = (int)(blockDim.x >> 6) / P;       // groups of 16 outputs in this workgroup
+    using R = st::Ring<NM, XI>;
+    constexpr int NB = R::kFrag, NO = GATED ? NM / 2 : NM;      // NO: groups of 16 outputs
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int G = (int)(blockDim.x >> 6) / P;       // output groups in this workgroup
     const int g = wave / P, p = wave - g * P;
-    const int units = (a.N + 15) / 16;
+    const int units = (a.N + 16 * NO - 1) / (16 * NO);
     const int u0 = blockIdx.x * G;
-    const int li = lane & 15, kq = 8 * (lane >> 4);
 
     floatx4 acc[NM][NB];
 #pragma unroll
     for (int m = 0; m < NM; ++m)
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[m][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-    const int s0 = p * slice, s1 = min(s0 + slice, (a.K + 31) / 32);
-    if (u0 + g < units && s0 < s1) {
-        // outputs past N and tokens past T repeat the last one; they are not stored
-        const int row = min(16 * (u0 + g) + li, a.N - 1);
-        const uint16_t *w[NM], *x[NB];
-        w[0] = a.w + (size_t)row * a.K + kq;
-        if constexpr (NM == 2) w[1] = a.wg + (size_t)row * a.K + kq;
+    const int blocks = (a.K + 63) / 64, b0 = p * slice, b1 = min(b0 + slice, blocks);
+    if (u0 + g < units && b0 < b1) {
+        const int r = st::copy_row(lane), k = 64 * b0 + st::copy_k(lane);
+        const uint16_t *src[R::kCopies];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) x[j] = a.x + (size_t)min(16 * j + li, a.T - 1) * a.xs + kq;
-        st::stream<BF16, NM, NB, 1, U>(acc, w, x, s0, s1, a.K, kq);
+        for (int i = 0; i < 2 * NM; ++i) {
+            const bool gate = GATED && i >= NM;
+            const int n = min(16 * NO * (u0 + g) + 8 * (gate ? i - NM : i) + r, a.N - 1);
+            src[i] = (gate ? a.wg : a.w) + (size_t)n * a.K + k;
+        }
+#pragma unroll
+        for (int i = 0; i < XI; ++i) src[2 * NM + i] = a.x + (size_t)min(8 * i + r, a.T - 1) * a.xs + k;
+        st::stream<BF16, NM, XI, D>(acc, smem + wave * D * R::kBlock, src, b1 - b0,
+                                    b1 == blocks ? a.K - 64 * (blocks - 1) : 64, lane);
     }
+    __syncthreads();                                // the rings are done with
+    float *red = (float *)smem;                     // [waves][NM][NB][64 lanes][4]
 #pragma unroll
     for (int m = 0; m < NM; ++m)
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             *(floatx4 *)&red[((wave * NM + m) * NB + j) * 256 + 4 * lane] = acc[m][j];
     __syncthreads();
-    for (int i = tid; i < G * NB * 256; i += blockDim.x) {
-        const int gg = i / (NB * 256), e = i - gg * NB * 256;
-        const int t = e >> 4, r = e & 15;           // token, output of the group
-        const int n = 16 * (u0 + gg) + r;
+    for (int i = tid; i < G * NO * NB * 256; i += blockDim.x) {
+        const int gg = i / (NO * NB * 256), e = i - gg * NO * NB * 256;
+        const int t = e / (16 * NO), o = e - t * 16 * NO;       // token, output of the group
+        const int n = 16 * NO * (u0 + gg) + o;
         if (t >= a.T || n >= a.N) continue;
+        const int r = o & 15;
         const int at = (t >> 4) * 256 + 4 * ((t & 15) + 16 * (r >> 2)) + (r & 3);
-        float v[2] = {0.f, 0.f};
-        for (int q = 0; q < P; ++q)
-#pragma unroll
-            for (int m = 0; m < NM; ++m) v[m] += red[((gg * P + q) * NM + m) * NB * 256 + at];
-        le::finish(a, t, n, v[0], v[1]);
+        float v = 0.f, g2 = 0.f;
+        for (int q = 0; q < P; ++q) {
+            const float *pr = red + ((gg * P + q) * NM + (o >> 4)) * NB * 256 + at;
+            v += pr[0];
+            if (GATED) g2 += pr[NO * NB * 256];
+        }
+        le::finish(a, t, n, v, g2);
     }
 }
 
-template <bool BF16, int NM, int NB>
-hipError_t launch_nb(const LinearArgs &a, hipStream_t s)
+template <bool BF16, bool GATED, int NM, int XI, int D>
+hipError_t launch_one(const LinearArgs &a, hipStream_t s)
 {
-    constexpr int U = NM * NB == 4 ? 4 : 8;
-    const int units = (a.N + 15) / 16, steps = (a.K + 31) / 32;
-    // slices of K: until there are about 4096 waves (16 per compute unit), while
-    // a slice keeps a full batch of steps
-    int P = 1;
-    while (P < 16 && (long long)units * P < 4096 && steps >= 2 * U * P) P *= 2;
-    int G = 1;
-    while (G * P < 4) G *= 2;                       // at least 4 waves per workgroup
-    const int slice = (steps + P - 1) / P;
-    const unsigned grid = (unsigned)((units + G - 1) / G);
-    const size_t lds = (size_t)G * P * NM * NB * 1024;
-    hipLaunchKernelGGL((linear_stream_kernel<BF16, NM, NB, U>), dim3(grid), dim3(64 * G * P), lds, s, a, P, slice);
+    using R = st::Ring<NM, XI>;
+    constexpr int NO = GATED ? NM / 2 : NM;
+    const int units = (a.N + 16 * NO - 1) / (16 * NO), blocks = (a.K + 63) / 64;
+    // slices of K: 4, more while the waves are too few to fill the chip and a
+    // slice keeps 4 blocks; fewer when K is short
+    int P = 4;
+    while (P < 8 && (long long)units * P < 2048 && blocks >= 8 * P) P *= 2;
+    while (P > 1 && blocks < P) P /= 2;
+    const int G = P < 4 ? 4 / P : 1, slice = (blocks + P - 1) / P;
+    constexpr int ring = D * R::kBlock, red = NM * R::kFrag * 1024;
+    const int lds = G * P * (ring > red ? ring : red);
+    const void *k = (const void *)linear_stream_kernel<BF16, GATED, NM, XI, D>;
+    if (lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((linear_stream_kernel<BF16, GATED, NM, XI, D>), dim3((unsigned)((units + G - 1) / G)),
+                       dim3(64 * G * P), lds, s, a, P, slice);
     return hipGetLastError();
+}
+
+// Rows per wave: 16 (and 16 of Wg).  From 17 tokens a block of tokens is larger
+// than that of 16 rows, so wide layers take 32 + 32 or 64.
+template <bool BF16, int XI>
+hipError_t launch_xi(const LinearArgs &a, hipStream_t s)
+{
+    constexpr int D = XI <= 2 ? 4 : 3;
+    if constexpr (XI > 2)
+        if (a.N >= 16384)
+            return a.wg ? launch_one<BF16, true, 4, XI, 3>(a, s) : launch_one<BF16, false, 4, XI, 3>(a, s);
+    return a.wg ? launch_one<BF16, true, 2, XI, 3>(a, s) : launch_one<BF16, false, 1, XI, D>(a, s);
 }
 
 template <bool BF16>
 hipError_t launch_t(const LinearArgs &a, hipStream_t s)
 {
-    if (a.T <= 16) return a.wg ? launch_nb<BF16, 2, 1>(a, s) : launch_nb<BF16, 1, 1>(a, s);
-    return a.wg ? launch_nb<BF16, 2, 2>(a, s) : launch_nb<BF16, 1, 2>(a, s);
+    if (a.T <= 8) return launch_xi<BF16, 1>(a, s);
+    if (a.T <= 16) return launch_xi<BF16, 2>(a, s);
+    if (a.T <= 24) return launch_xi<BF16, 3>(a, s);
+    return launch_xi<BF16, 4>(a, s);
 }
 
 }  // namespace

@@ -18,9 +18,6 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr int kKB = 64;                             // k values per block: 128-byte rows
 
-// Read in place of k values past the end of the rows
-__device__ __align__(16) const uint16_t zeros16[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-
 template <bool BF16>
 __device__ __forceinline__ floatx16 mma32(const uint4 &a, const uint4 &b, const floatx16 &c)
 {
@@ -92,7 +89,7 @@ linear_tile_kernel(LinearArgs a, Cut c)
         } else {
 #pragma unroll
             for (int q = 0; q < NI; ++q)
-                copy16_to_lds(kb * kKB + ch[q] < a.K ? src[q] + (size_t)kb * kKB : zeros16,
+                copy16_to_lds(kb * kKB + ch[q] < a.K ? src[q] + (size_t)kb * kKB : st::zeros16,
                               base + 1024 * (wave + W * q));
         }
     };
