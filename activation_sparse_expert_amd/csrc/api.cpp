@@ -442,17 +442,17 @@ bool few_size_ok(int T, int d, int f, int E, int k, int S)
 }
 
 struct FewWs {
-    float *lg;
+    float *lg, *part;
     FewTab tab;
     uint16_t *h;
 };
 
-int few_amax(int T, int E, int k, int S) { return (E < T * k ? E : T * k) + S; }
-
-size_t few_ws_bytes(int T, int f, int E, int k, int S, FewWs *out, void *base)
+size_t few_ws_bytes(int T, int d, int f, int E, int k, int S, FewWs *out, void *base)
 {
     const size_t rows = (size_t)T * (k + S), amax = few_amax(T, E, k, S);
-    const size_t size[7] = {(size_t)T * E * 4, 4, amax * 4, (amax + 1) * 4, rows * 4, rows * 4, rows * f * 4};
+    const size_t parts = few_parts(T, d, f, E, k, S);
+    const size_t size[7] = {(size_t)T * E * 4, 4, amax * 16, rows * 4, rows * f * 4, (size_t)(d + 15) / 16 * 4,
+                            parts * T * d * 4};
     size_t off[7], o = 0;
     for (int i = 0; i < 7; ++i) {
         off[i] = o;
@@ -462,11 +462,11 @@ size_t few_ws_bytes(int T, int f, int E, int k, int S, FewWs *out, void *base)
         char *p = (char *)base;
         out->lg = (float *)(p + off[0]);
         out->tab.n = (int32_t *)(p + off[1]);
-        out->tab.expert = (int32_t *)(p + off[2]);
-        out->tab.off = (int32_t *)(p + off[3]);
-        out->tab.tok = (int32_t *)(p + off[4]);
-        out->tab.wt = (float *)(p + off[5]);
-        out->h = (uint16_t *)(p + off[6]);
+        out->tab.rec = (int4 *)(p + off[2]);
+        out->tab.wt = (float *)(p + off[3]);
+        out->h = (uint16_t *)(p + off[4]);
+        out->tab.done = (int32_t *)(p + off[5]);
+        out->part = (float *)(p + off[6]);
     }
     return o;
 }
@@ -524,7 +524,7 @@ size_t moe_workspace_size(moe_op op, int T, int d, int f, int E, int k, int S)
     case MOE_OP_LINEAR:
         return linear_size_ok(T, d, f) ? linear_ws_bytes(T, d, f) : 0;
     case MOE_OP_LAYER_FEW:
-        return few_size_ok(T, d, f, E, k, S) ? few_ws_bytes(T, f, E, k, S, nullptr, nullptr) : 0;
+        return few_size_ok(T, d, f, E, k, S) ? few_ws_bytes(T, d, f, E, k, S, nullptr, nullptr) : 0;
     }
     return 0;
 }
@@ -971,35 +971,27 @@ moe_status moe_layer_forward_few(const moe_layer *L, const void *x, moe_dtype xd
             !aligned(trace->expert_count, 4) || !aligned(trace->eam_row, 4))
             return MOE_ERR_ALIGNMENT;
     }
-    if (!ws || ws_bytes < few_ws_bytes(T, f, E, k, S, nullptr, nullptr)) return MOE_ERR_WORKSPACE;
+    if (!ws || ws_bytes < few_ws_bytes(T, d, f, E, k, S, nullptr, nullptr)) return MOE_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return MOE_ERR_ALIGNMENT;
 
     hipStream_t s = (hipStream_t)stream;
     FewWs w;
-    few_ws_bytes(T, f, E, k, S, &w, ws);
-    RouteArgs r{};
-    r.x = x; r.xdt = xdt; r.T = T; r.d = d;
-    r.rw = L->router_w; r.rdt = L->rdt; r.bias = L->router_bias;
-    r.E = E;
-    r.lg_buf = w.lg;
-    hipError_t he = launch_route_logits(r, s);
-    if (he != hipSuccess) return MOE_ERR_HIP;
+    few_ws_bytes(T, d, f, E, k, S, &w, ws);
     FewArgs a{};
     a.T = T; a.d = d; a.f = f; a.E = E; a.k = k; a.S = S;
     a.bf16 = L->wdt == MOE_BF16 ? 1 : 0; a.ydt = (int)ydt;
     a.x = (const uint16_t *)x;
     a.gate = (const uint16_t *)L->gate_t; a.up = L->up_dense; a.down_t = (const uint16_t *)L->down_dense;
-    a.lg = w.lg; a.renorm = L->renormalize ? 1 : 0;
+    a.rw = L->router_w; a.rdt = (int)L->rdt; a.rbias = L->router_bias;
+    a.renorm = L->renormalize ? 1 : 0;
+    a.lg = w.lg; a.part = w.part;
     a.tab = w.tab; a.amax = few_amax(T, E, k, S); a.h = w.h;
     a.r = residual; a.y = y;
     if (trace) {
         a.topk_idx = trace->topk_idx; a.topk_w = trace->topk_w; a.logits = trace->logits;
         a.count = trace->expert_count; a.eam_row = trace->eam_row; a.expert_dense = trace->expert_dense;
     }
-    he = launch_few_rank(a, s);
-    if (he == hipSuccess) he = launch_few_gateup(a, s);
-    if (he == hipSuccess) he = launch_few_down(a, s);
-    return hip_status(he);
+    return hip_status(launch_few(a, s));
 }
 
 moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt, long long x_stride,

@@ -32,13 +32,12 @@ size_t linear_tile_ws_bytes(int T, int K, int N);       // the larger of the pla
 
 // The few-token MoE layer: the experts of a call and their tokens, made from the
 // routing once.  Experts with tokens are listed in ascending order, the shared ones
-// last; expert i's tokens are rows off[i] .. off[i + 1] - 1, ascending.
+// last; an expert's tokens have consecutive rows.
 struct FewTab {
     int32_t *n;                         // [1] experts listed
-    int32_t *expert;                    // [A]
-    int32_t *off;                       // [A + 1]
-    int32_t *tok;                       // [T (k + S)] token of each row
-    float *wt;                          // [T (k + S)] its router weight (shared experts: 1)
+    int4 *rec;                          // [A] {expert (-1 past the list), token bits, first row, -}
+    float *wt;                          // [T (k + S)] router weight of each row (shared experts: 1)
+    int32_t *done;                      // [ceil(d / 16)] parts of a column block that are written
 };
 
 struct FewArgs {
@@ -47,11 +46,15 @@ struct FewArgs {
     const uint16_t *x;                  // [T][d]
     const uint16_t *gate, *up;          // [E+S][f][d]
     const uint16_t *down_t;             // [E+S][d][f]
-    const float *lg;                    // [T][E] router logits
+    const void *rw;                     // [E][d] router in rdt
+    int rdt;
+    const float *rbias;                 // [E] or null
     int renorm;
+    float *lg;                          // [T][E] logits (workspace)
     FewTab tab;
     int amax;                           // bound of the listed experts: min(E, T k) + S
     uint16_t *h;                        // [T (k + S)][hi, lo][f] (workspace)
+    float *part;                        // [few_parts][T][d] (workspace)
     const void *r;                      // [T][d] or null
     void *y;                            // [T][d]
     int32_t *topk_idx;                  // trace exports or null
@@ -62,8 +65,8 @@ struct FewArgs {
 
 constexpr int kFewTokens = 32;
 constexpr int kFewRows = 2048;          // T (k + S)
-hipError_t launch_few_rank(const FewArgs &a, hipStream_t s);
-hipError_t launch_few_gateup(const FewArgs &a, hipStream_t s);
-hipError_t launch_few_down(const FewArgs &a, hipStream_t s);
+int few_amax(int T, int E, int k, int S);
+int few_parts(int T, int d, int f, int E, int k, int S);
+hipError_t launch_few(const FewArgs &a, hipStream_t s);
 
 }  // namespace moeffn
