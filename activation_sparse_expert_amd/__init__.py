@@ -7,6 +7,7 @@ stream.  If the shared library has not been built, every call raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -353,17 +354,18 @@ def layer_forward(layer: Layer, x, *, path: int = PATH_SPARSE, y=None, out_dtype
     return y
 
 
-def _on(x, **others):
-    """Checks that the tensors of a call lie on x's GPU (None allowed)."""
-    if x.device.type != "cuda":
-        raise ValueError("x must be a GPU tensor")
-    for name, t in others.items():
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+@functools.lru_cache(maxsize=1024)
+def _size_of(op: int, T: int, d: int, f: int, E: int, k: int, S: int) -> int:
+    return workspace_size(op, T, d, f, E, k, S)
 
 
-def _shaped(name, t, shape, dtype=None):
-    if tuple(t.shape) != tuple(shape):
+def _want(name, t, device, shape, dtype=None):
+    """Checks that t, unless None, lies on the call's GPU with this shape (and type)."""
+    if t is None:
+        return
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, x on {device}")
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -372,13 +374,36 @@ def _shaped(name, t, shape, dtype=None):
 def _rows(name, t, align=1):
     """(data pointer, row stride) of a matrix whose rows are contiguous.  The
     stride of a single row means nothing and is taken as the row's length."""
-    if t is None:
-        return None, 0
-    n = t.shape[1]
-    if t.stride(1) != 1 and n > 1:
+    T, n = t.shape
+    rs, cs = t.stride()
+    if cs != 1 and n > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    stride = t.stride(0) if t.shape[0] > 1 else (n + align - 1) // align * align
-    return t.data_ptr(), stride
+    return t.data_ptr(), rs if T > 1 else (n + align - 1) // align * align
+
+
+def _workspace(torch, device, nbytes, ws):
+    """(pointer, bytes) of a call's workspace: the caller's, or one from
+    torch's allocator (not initialised), or none where the call needs none."""
+    if ws is not None:
+        if ws.device != device:
+            raise ValueError(f"ws is on {ws.device}, x on {device}")
+        return ws, _ptr(ws), ws.numel() * ws.element_size()
+    if not nbytes:
+        return None, None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), nbytes
+
+
+def _call(torch, device, what, fn, *args):
+    """fn(*args, stream) on the device's current stream, with the device current."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != 0:
+        raise MoeError(st, what)
 
 
 _TRACE_DTYPES = {"topk_idx": "int32", "topk_w": "float32", "logits": "float32", "expert_count": "int32",
@@ -398,42 +423,44 @@ def layer_forward_few(layer: Layer, x, *, residual=None, y=None, out_dtype=None,
     import torch
     if x.dim() != 2:
         raise ValueError("x must be [T][d]")
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
     T, d = x.shape
     E, S, f, k = layer.E, layer.S, layer.f, layer.k
-    trace = trace or {}
-    _on(x, residual=residual, y=y, ws=ws, router_w=layer.router_w, router_bias=layer.router_bias,
-        gate_t=layer.gate_t, up_dense=layer.up_dense, down_dense=layer.down_dense, **trace)
-    _shaped("x", x, (T, layer.d))
-    if layer.up_dense is None or layer.down_dense is None:
+    gate, up, down = layer.gate_t, layer.up_dense, layer.down_dense
+    if up is None or down is None:
         raise ValueError("the layer needs up_dense and down_dense")
-    _shaped("router_w", layer.router_w, (E, d))
-    if layer.router_bias is not None:
-        _shaped("router_bias", layer.router_bias, (E,), torch.float32)
-    _shaped("gate_t", layer.gate_t, (E + S, f, d))
-    _shaped("up_dense", layer.up_dense, (E + S, f, d), layer.gate_t.dtype)
-    _shaped("down_dense", layer.down_dense, (E + S, d, f), layer.gate_t.dtype)
+    if d != layer.d:
+        raise ValueError(f"x has {d} columns, the layer d = {layer.d}")
+    wdt = gate.dtype
+    _want("router_w", layer.router_w, device, (E, d))
+    _want("router_bias", layer.router_bias, device, (E,), torch.float32)
+    _want("gate_t", gate, device, (E + S, f, d))
+    _want("up_dense", up, device, (E + S, f, d), wdt)
+    _want("down_dense", down, device, (E + S, d, f), wdt)
     if y is None:
-        y = torch.empty((T, d), dtype=out_dtype or torch.float32, device=x.device)
-    _shaped("y", y, (T, d))
-    if residual is not None:
-        _shaped("residual", residual, (T, d), y.dtype)
-    shapes = {"topk_idx": (T, k), "topk_w": (T, k), "logits": (T, E)}
-    for name, t in trace.items():
-        if t is None:
-            continue
-        if name not in _TRACE_DTYPES:
-            raise ValueError(f"layer_forward_few exports no {name}")
-        _shaped(name, t, shapes.get(name, (E,)), getattr(torch, _TRACE_DTYPES[name]))
-    with torch.cuda.device(x.device):
-        if ws is None:
-            ws = torch.empty(max(256, workspace_size(OP_LAYER_FEW, T, d, f, E, k, S)),
-                             dtype=torch.uint8, device=x.device)
-        tr = LayerTrace(**{name: _ptr(t) for name, t in trace.items()}) if trace else None
-        desc = layer.desc()
-        st = lib().moe_layer_forward_few(C.byref(desc), _ptr(x), _dt(x), T, _ptr(residual), _ptr(y),
-                                         _dt(y), C.byref(tr) if tr is not None else None, _ptr(ws),
-                                         ws.numel() * ws.element_size(), _stream())
-    _check(st, "moe_layer_forward_few")
+        y = torch.empty((T, d), dtype=out_dtype or torch.float32, device=device)
+    else:
+        _want("y", y, device, (T, d))
+    _want("residual", residual, device, (T, d), y.dtype)
+    tr = None
+    if trace:
+        for name, t in trace.items():
+            if name not in _TRACE_DTYPES:
+                if t is None:
+                    continue
+                raise ValueError(f"layer_forward_few exports no {name}")
+            shape = (T, k) if name[:4] == "topk" else (T, E) if name == "logits" else (E,)
+            _want(name, t, device, shape, getattr(torch, _TRACE_DTYPES[name]))
+        tr = C.byref(LayerTrace(**{name: _ptr(t) for name, t in trace.items() if t is not None}))
+    ws, wp, wb = _workspace(torch, device, _size_of(OP_LAYER_FEW, T, d, f, E, k, S), ws)
+    desc = LayerDesc(d=d, f=f, n_routed=E, n_shared=S, top_k=k, renormalize=int(bool(layer.renormalize)),
+                     wdt=_dt(gate), router_w=_ptr(layer.router_w), rdt=_dt(layer.router_w),
+                     router_bias=_ptr(layer.router_bias), gate_t=_ptr(gate), up_dense=_ptr(up),
+                     down_dense=_ptr(down))
+    _call(torch, device, "moe_layer_forward_few", lib().moe_layer_forward_few, C.byref(desc), _ptr(x),
+          _dt(x), T, _ptr(residual), _ptr(y), _dt(y), tr, wp, wb)
     return y
 
 
@@ -458,7 +485,7 @@ class Linear:
     def desc(self) -> LinearDesc:
         if self.act not in ACT:
             raise ValueError(f"act must be one of {sorted(ACT)}")
-        return LinearDesc(self.n, self.k, _dt(self.w), _ptr(self.w), _ptr(self.bias),
+        return LinearDesc(self.w.shape[0], self.w.shape[1], _dt(self.w), _ptr(self.w), _ptr(self.bias),
                           _ptr(self.w_gate), _ptr(self.bias_gate), ACT[self.act])
 
 
@@ -470,32 +497,27 @@ def linear_forward(linear: Linear, x, *, residual=None, y=None, out_dtype=None, 
     import torch
     if x.dim() != 2:
         raise ValueError("x must be [T][k]")
-    T, (n, k) = x.shape[0], linear.w.shape
-    _on(x, residual=residual, y=y, ws=ws, w=linear.w, bias=linear.bias, w_gate=linear.w_gate,
-        bias_gate=linear.bias_gate)
-    _shaped("x", x, (T, k))
-    for name in ("bias", "bias_gate"):
-        t = getattr(linear, name)
-        if t is not None:
-            _shaped(name, t, (n,), torch.float32)
-    if linear.w_gate is not None:
-        _shaped("w_gate", linear.w_gate, (n, k), linear.w.dtype)
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    w = linear.w
+    T, (n, k) = x.shape[0], w.shape
+    _want("x", x, device, (T, k))
+    _want("w", w, device, (n, k))
+    _want("bias", linear.bias, device, (n,), torch.float32)
+    _want("w_gate", linear.w_gate, device, (n, k), w.dtype)
+    _want("bias_gate", linear.bias_gate, device, (n,), torch.float32)
     if y is None:
-        y = torch.empty((T, n), dtype=out_dtype or torch.float32, device=x.device)
-    _shaped("y", y, (T, n))
-    if residual is not None:
-        _shaped("residual", residual, (T, n), y.dtype)
+        y = torch.empty((T, n), dtype=out_dtype or torch.float32, device=device)
+    else:
+        _want("y", y, device, (T, n))
+    _want("residual", residual, device, (T, n), y.dtype)
     xp, xs = _rows("x", x, 8)
     yp, ys = _rows("y", y)
-    rp, rs = _rows("residual", residual)
-    with torch.cuda.device(x.device):
-        if ws is None:
-            ws = torch.empty(max(256, workspace_size(OP_LINEAR, T, k, n)), dtype=torch.uint8,
-                             device=x.device)
-        desc = linear.desc()
-        st = lib().moe_linear_forward(C.byref(desc), xp, _dt(x), xs, T, rp, rs, yp, _dt(y), ys,
-                                      _ptr(ws), ws.numel() * ws.element_size(), _stream())
-    _check(st, "moe_linear_forward")
+    rp, rs = _rows("residual", residual) if residual is not None else (None, 0)
+    ws, wp, wb = _workspace(torch, device, _size_of(OP_LINEAR, T, k, n, 0, 0, 0), ws)
+    _call(torch, device, "moe_linear_forward", lib().moe_linear_forward, C.byref(linear.desc()), xp,
+          _dt(x), xs, T, rp, rs, yp, _dt(y), ys, wp, wb)
     return y
 
 

@@ -432,7 +432,7 @@ bool linear_size_ok(int T, int k, int n)
 
 size_t linear_ws_bytes(int T, int k, int n)
 {
-    return T <= kStreamTokens ? kAlign : up(linear_tile_ws_bytes(T, k, n)) + kAlign;
+    return T <= kStreamTokens ? 0 : up(linear_tile_ws_bytes(T, k, n));
 }
 
 bool few_size_ok(int T, int d, int f, int E, int k, int S)
@@ -451,7 +451,7 @@ size_t few_ws_bytes(int T, int d, int f, int E, int k, int S, FewWs *out, void *
 {
     const size_t rows = (size_t)T * (k + S), amax = few_amax(T, E, k, S);
     const size_t parts = few_parts(T, d, f, E, k, S);
-    const size_t size[7] = {(size_t)T * E * 4, 4, amax * 16, rows * 4, rows * f * 4, (size_t)(d + 15) / 16 * 4,
+    const size_t size[7] = {(size_t)T * E * 4, 4, (amax + 1) * 16, rows * 4, rows * f * 4, (size_t)(d + 15) / 16 * 4,
                             parts * T * d * 4};
     size_t off[7], o = 0;
     for (int i = 0; i < 7; ++i) {
@@ -1011,7 +1011,8 @@ moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt,
     if (!aligned(x, 16) || x_stride % 8 != 0 || !aligned(L->w, 16) || !aligned(L->w_gate, 16) || !aligned(y, ya) ||
         !aligned(residual, ya) || !aligned(L->bias, 4) || !aligned(L->bias_gate, 4))
         return MOE_ERR_ALIGNMENT;
-    if (!ws || ws_bytes < linear_ws_bytes(T, k, n)) return MOE_ERR_WORKSPACE;
+    const size_t need = linear_ws_bytes(T, k, n);
+    if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return MOE_ERR_ALIGNMENT;
     LinearArgs a{};
     a.T = T; a.K = k; a.N = n;

@@ -28,12 +28,108 @@ namespace {
 
 using st::floatx4;
 
-// A listed expert, one 16-byte load: {expert or -1, its tokens as bits, first row, -}.
-// Its r-th token is the r-th set bit and has row first + r.
+// A listed expert, one 16-byte load: {expert or -1, its tokens as bits, first row,
+// down_cost of the experts before it}.  Its r-th token is the r-th set bit and has row
+// first + r.
 __device__ __forceinline__ int nth_bit(uint32_t mask, int r)
 {
     for (; r > 0; --r) mask &= mask - 1;
     return __ffs(mask) - 1;
+}
+
+// What a block of an expert with n tokens costs in the down product, in half KB of
+// weights copied from HBM and, at half the price, of hi and lo rows from L2.
+__device__ __forceinline__ int down_cost(int n)
+{
+    auto pass = [](int m) { return m <= 4 ? 5 : m <= 8 ? 6 : 8; };
+    return n <= 16 ? pass(n) : 8 + pass(n - 16);
+}
+
+// The largest of the wave's 64 values, in every lane
+__device__ __forceinline__ float wave_max(float v)
+{
+    // lanes l ^ 1, l ^ 2, then the mirror images within 8 and 16 lanes, then rows
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, false)));
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, false)));
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, false)));
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, false)));
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// The k best of E <= 64 N experts by one wave, in registers, in the order that
+// rank_topk ranks by: larger logit, then lower index, NaN as -inf.  emit(s, e)
+// gets them best first; took[j] are the experts 64 j + bit among them.  k rounds
+// of an arg-max over the lanes: for a few choices far fewer instructions than
+// counting, for each expert, those ahead of it.
+constexpr int kSelect = 16;                         // choices up to which this is the shorter way
+template <int N, class F>
+__device__ __forceinline__ void select(const float *lg, int E, int k, int lane, unsigned long long (&took)[N], F emit)
+{
+    float v[N];                                     // logit of expert 64 j + lane
+    bool left[N];                                   // and whether it may still be chosen
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int e = lane + 64 * j;
+        left[j] = e < E;
+        took[j] = 0ull;
+        const float l = left[j] ? lg[e] : -INFINITY;
+        v[j] = l != l ? -INFINITY : l;
+    }
+    for (int s = 0; s < k; ++s) {
+        float best = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < N; ++j) best = fmaxf(best, left[j] ? v[j] : -INFINITY);
+        best = wave_max(best);
+        int e = -1;
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j) {          // the lowest that has it
+            const unsigned long long b = __ballot(left[j] && v[j] == best);
+            e = b ? 64 * j + __ffsll(b) - 1 : e;
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const bool it = e == 64 * j + lane;
+            left[j] = left[j] && !it;
+            took[j] |= __ballot(it);
+        }
+        emit(s, e);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void select_to(const float *lg, int E, int k, int lane, int *to)
+{
+    unsigned long long took[N];
+    select<N>(lg, E, k, lane, took, [&](int s, int e) { if (lane == 0) to[s] = e; });
+}
+
+// One token: the i-th in ascending order of its k <= kSelect best experts
+template <int N>
+__device__ __forceinline__ int pick_of(const float *lg, int E, int k, int i, int lane)
+{
+    unsigned long long took[N];
+    select<N>(lg, E, k, lane, took, [](int, int) {});
+    int e = -1;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int c = __popcll(took[j]);
+        if (e < 0 && i < c) {
+            unsigned long long b = took[j];
+            for (; i > 0; --i) b &= b - 1;
+            e = 64 * j + __ffsll(b) - 1;
+        }
+        i -= c;
+    }
+    return e;
+}
+
+__device__ __forceinline__ int pick(const float *lg, int E, int k, int i, int lane)
+{
+    if (E <= 64) return pick_of<1>(lg, E, k, i, lane);
+    return E <= 256 ? pick_of<4>(lg, E, k, i, lane) : pick_of<16>(lg, E, k, i, lane);
 }
 
 // Bytes of LDS that route() works in
@@ -43,7 +139,7 @@ __host__ __device__ inline size_t route_bytes(int T, int E, int k)
 }
 
 // Ranks the logits and lists the experts, by one workgroup.  LOGITS: forms the
-// logits too.  rec [amax] (LDS or global); wt: the rows' router weights, or null
+// logits too.  rec [amax + 1] (LDS or global); wt: the rows' router weights, or null
 // where another workgroup writes them with the call's exports.
 template <bool BF16, bool LOGITS>
 __device__ void route(const FewArgs &a, int4 *rec, unsigned char *smem, bool exports)
@@ -71,7 +167,13 @@ __device__ void route(const FewArgs &a, int4 *rec, unsigned char *smem, bool exp
         }
     }
     __syncthreads();
-    for (int t = wave; t < a.T; t += waves) rc::rank_topk(lg + t * E4, E, k, sel + t * k, lane, 64);
+    for (int t = wave; t < a.T; t += waves) {
+        int *to = sel + t * k;
+        if (k > kSelect) rc::rank_topk(lg + t * E4, E, k, to, lane, 64);
+        else if (E <= 64) select_to<1>(lg + t * E4, E, k, lane, to);
+        else if (E <= 256) select_to<4>(lg + t * E4, E, k, lane, to);
+        else select_to<16>(lg + t * E4, E, k, lane, to);
+    }
     __syncthreads();
     for (int t = wave; t < a.T; t += waves) {
         const float *row = lg + t * E4;
@@ -84,28 +186,33 @@ __device__ void route(const FewArgs &a, int4 *rec, unsigned char *smem, bool exp
     }
     __syncthreads();
     if (wave == 0) {
-        int na = 0, rows = 0;
+        int na = 0, rows = 0, cost = 0;
         for (int e0 = 0; e0 < E; e0 += 64) {
             const uint32_t m = e0 + lane < E ? em[e0 + lane] : 0u;
             const unsigned long long b = __ballot(m != 0u);
-            const int c = __popc(m);
-            int incl = c;
+            // rows (at most 32 x 64 here) and costs, scanned together
+            const int c = __popc(m), v0 = c | (m ? down_cost(c) : 0) << 16;
+            int incl = v0;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
                 const int v = __shfl_up(incl, o, 64);
                 if (lane >= o) incl += v;
             }
             if (m) {
-                rec[na + __popcll(b & ((1ull << lane) - 1ull))] = make_int4(e0 + lane, (int)m, rows + incl - c, 0);
-                eo[e0 + lane] = rows + incl - c;
+                const int off = rows + ((incl - v0) & 0xFFFF);
+                rec[na + __popcll(b & ((1ull << lane) - 1ull))] = make_int4(e0 + lane, (int)m, off, cost + ((incl - v0) >> 16));
+                eo[e0 + lane] = off;
             }
             na += __popcll(b);
-            rows += __shfl(incl, 63, 64);
+            const int sum = __shfl(incl, 63, 64);
+            rows += sum & 0xFFFF;
+            cost += sum >> 16;
         }
         const uint32_t all = 0xFFFFFFFFu >> (32 - a.T);
-        for (int i = na + lane; i < a.amax; i += 64) {
+        for (int i = na + lane; i <= a.amax; i += 64) {
             const int sh = i - na;
-            rec[i] = sh < a.S ? make_int4(E + sh, (int)all, rows + sh * a.T, 0) : make_int4(-1, 0, 0, 0);
+            const int w = cost + min(sh, a.S) * down_cost(a.T);
+            rec[i] = sh < a.S ? make_int4(E + sh, (int)all, rows + sh * a.T, w) : make_int4(-1, 0, 0, w);
         }
         if (lane == 0) *count = na + a.S;
     }
@@ -139,62 +246,13 @@ few_rank_kernel(FewArgs a)
     route<false, false>(a, a.tab.rec, smem, true);
 }
 
-// One token, E <= 64 kPickLanes: the i-th in ascending order of its k best experts, found by each
-// wave in registers (k rounds of an arg-max over the lanes), in the order that
-// rank_topk ranks by: larger logit, then lower index; NaN as -inf, -0 as 0.
-constexpr int kPick = 8;                            // logits per lane
-__device__ __forceinline__ int pick(const float *lg, int E, int k, int i, int lane)
-{
-    unsigned long long key[kPick];
-#pragma unroll
-    for (int j = 0; j < kPick; ++j) {
-        const int e = lane + 64 * j;
-        key[j] = 0ull;                              // below every expert
-        if (64 * j < E && e < E) {
-            float v = lg[e];
-            v = v != v ? -INFINITY : v + 0.f;
-            const uint32_t b = __float_as_uint(v);
-            key[j] = (unsigned long long)((b & 0x80000000u) ? ~b : b | 0x80000000u) << 32 | (0xFFFFFFFFu - (uint32_t)e);
-        }
-    }
-    uint32_t took = 0u;
-    for (int s = 0; s < k; ++s) {
-        unsigned long long best = key[0];
-#pragma unroll
-        for (int j = 1; j < kPick; ++j) best = key[j] > best ? key[j] : best;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const unsigned long long v = __shfl_xor(best, o, 64);
-            best = v > best ? v : best;
-        }
-#pragma unroll
-        for (int j = 0; j < kPick; ++j)
-            if (key[j] == best) {
-                key[j] = 0ull;
-                took |= 1u << j;
-            }
-    }
-    int e = -1;
-#pragma unroll
-    for (int j = 0; j < kPick; ++j) {
-        unsigned long long b = __ballot((took >> j) & 1u);
-        const int c = __popcll(b);
-        if (e < 0 && i < c) {
-            for (; i > 0; --i) b &= b - 1;
-            e = 64 * j + __ffsll(b) - 1;
-        }
-        i -= c;
-    }
-    return __builtin_amdgcn_readfirstlane(e);
-}
-
 // Gate and up products of one wave: 16 channels from c, the expert's n tokens (at
-// most 8 XI), blocks [b0, b1) of d.
-template <bool BF16, int XI, int D>
+// most XR), blocks [b0, b1) of d.
+template <bool BF16, int XR, int D>
 __device__ __forceinline__ void gateup_wave(const FewArgs &a, unsigned char *ring, int e, uint32_t mask, int n, int c,
                                             int b0, int b1, int blocks, int lane, floatx4 (&out)[2][2])
 {
-    using R = st::Ring<2, XI>;
+    using R = st::Ring<2, XR>;
     floatx4 acc[2][R::kFrag];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -208,29 +266,32 @@ __device__ __forceinline__ void gateup_wave(const FewArgs &a, unsigned char *rin
         src[i] = (i < 2 ? a.gate : a.up) + ((size_t)e * a.f + ch) * a.d + k;
     }
 #pragma unroll
-    for (int i = 0; i < XI; ++i) src[4 + i] = a.x + (size_t)nth_bit(mask, min(8 * i + r, n - 1)) * a.d + k;
-    st::stream<BF16, 2, XI, D>(acc, ring, src, b1 - b0, b1 == blocks ? a.d - 64 * (blocks - 1) : 64, lane);
+    for (int i = 0; i < R::kTok; ++i) src[4 + i] = a.x + (size_t)nth_bit(mask, min(8 * i + r, n - 1)) * a.d + k;
+    st::stream<BF16, 2, XR, D>(acc, ring, src, b1 - b0, b1 == blocks ? a.d - 64 * (blocks - 1) : 64, lane);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int j = 0; j < R::kFrag; ++j) out[m][j] = acc[m][j];
 }
 
-// Bytes of a wave's ring, and its depth where blocks have XI token rows of 8
-constexpr int kUpRing(int xm) { return 3 * st::Ring<2, 1>::kBlock + (xm - 1) * 3 * 1024; }
-constexpr int kUpDepth(int xm, int xi) { return kUpRing(xm) / (1024 * (4 + xi)) < 4 ? kUpRing(xm) / (1024 * (4 + xi)) : 4; }
-constexpr int kDownRing(int xm) { return xm == 1 ? 12 * 1024 : xm == 2 ? 16 * 1024 : 18 * 1024; }
-constexpr int kDownDepth(int xm, int xi) { return kDownRing(xm) / (1024 * (2 + xi)); }
+// Bytes of a wave's ring in a kernel for at most xm token rows (hi and lo count
+// apart in the down product), and its depth where blocks hold xr of them: 3 or 4
+// blocks at xm rows, as many as fit with fewer.
+constexpr int kUpRing(int xm) { return 3 * (4096 + 128 * xm); }
+constexpr int kUpDepth(int xm, int xr) { return kUpRing(xm) / (4096 + 128 * xr); }
+constexpr int kDownM(int xm) { return xm <= 16 ? 1 : 2; }  // groups of 16 columns
+constexpr int kDownRing(int xm) { return 4 * (2048 * kDownM(xm) + 128 * xm); }
+constexpr int kDownDepth(int xm, int xr) { return kDownRing(xm) / (2048 * kDownM(xm) + 128 * xr); }
 
 // Where the gate/up kernel has the list from
 enum { kFromList = 0, kFromLogits = 1, kFromRouter = 2 };
 
-// XM: groups of 8 tokens that an expert can have (1, 2 or 4); P waves share 16 channels
+// XM: tokens that an expert can have (1, 8, 16 or 32); P waves share 16 channels
 template <bool BF16, int XM, int ROUTE>
 __global__ void __launch_bounds__(512)
 few_gateup_kernel(FewArgs a, int P, int slice)
 {
-    constexpr int NB = (XM + 1) / 2;
+    constexpr int NB = (XM + 15) / 16;
     extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
@@ -241,10 +302,10 @@ few_gateup_kernel(FewArgs a, int P, int slice)
     const int4 *list = a.tab.rec;
     if constexpr (ROUTE == kFromRouter) {
         int4 *own = (int4 *)smem;
-        rings += 16 * (size_t)a.amax;
+        rings += 16 * (size_t)(a.amax + 1);
         route<BF16, true>(a, own, rings, blockIdx.x == 0);
         if (blockIdx.x == 0)
-            for (int i = tid; i < a.amax; i += blockDim.x) a.tab.rec[i] = own[i];
+            for (int i = tid; i <= a.amax; i += blockDim.x) a.tab.rec[i] = own[i];
         list = own;
     }
     if constexpr (ROUTE == kFromLogits) {
@@ -270,11 +331,13 @@ few_gateup_kernel(FewArgs a, int P, int slice)
         const int n = __popc(mask);
         unsigned char *ring = rings + wave * kUpRing(XM);
         if (e >= 0) {
-            if (XM == 1 || n <= 8)
-                gateup_wave<BF16, 1, kUpDepth(XM, 1)>(a, ring, e, mask, n, c, b0, b1, blocks, lane, acc);
-            else if (XM == 2 || n <= 16)
-                gateup_wave<BF16, 2, kUpDepth(XM, 2)>(a, ring, e, mask, n, c, b0, b1, blocks, lane, acc);
-            else gateup_wave<BF16, 4, kUpDepth(XM, 4)>(a, ring, e, mask, n, c, b0, b1, blocks, lane, acc);
+            if constexpr (XM == 1)
+                gateup_wave<BF16, 1, kUpDepth(1, 1)>(a, ring, e, mask, n, c, b0, b1, blocks, lane, acc);
+            else if (XM == 8 || n <= 8)
+                gateup_wave<BF16, 8, kUpDepth(XM, 8)>(a, ring, e, mask, n, c, b0, b1, blocks, lane, acc);
+            else if (XM == 16 || n <= 16)
+                gateup_wave<BF16, 16, kUpDepth(XM, 16)>(a, ring, e, mask, n, c, b0, b1, blocks, lane, acc);
+            else gateup_wave<BF16, 32, kUpDepth(XM, 32)>(a, ring, e, mask, n, c, b0, b1, blocks, lane, acc);
         }
     }
     __syncthreads();                                // the rings are done with
@@ -311,28 +374,30 @@ few_gateup_kernel(FewArgs a, int P, int slice)
     }
 }
 
-// One wave's share of one expert: 16 columns from col, blocks [b0, b1) of its
+// One wave's share of one expert: 16 NM columns from col, blocks [b0, b1) of its
 // channels, tokens first .. first + n - 1 of the expert's; the 2 n columns of the matrix
-// core are hi, then lo of the n tokens.  The weighted sum goes into y [T][16],
+// core are hi, then lo of the n tokens.  The weighted sum goes into y [T][16 NM],
 // this wave's own LDS.
-template <bool BF16, int XI, int D>
+template <bool BF16, int NM, int XR, int D>
 __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring, float *y, int4 rec, int first, int n,
                                           int col, int b0, int b1, int blocks, int lane)
 {
-    using R = st::Ring<1, XI>;
-    floatx4 acc[1][R::kFrag];
+    using R = st::Ring<NM, XR>;
+    floatx4 acc[NM][R::kFrag];
 #pragma unroll
-    for (int j = 0; j < R::kFrag; ++j) acc[0][j] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+        for (int j = 0; j < R::kFrag; ++j) acc[m][j] = floatx4{0.f, 0.f, 0.f, 0.f};
     const int off = rec.z + first;
     const int r = st::copy_row(lane), k = 64 * b0 + st::copy_k(lane);
     const uint16_t *src[R::kCopies];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2 * NM; ++i)
         src[i] = a.down_t + ((size_t)rec.x * a.d + min(col + 8 * i + r, a.d - 1)) * a.f + k;
 #pragma unroll
-    for (int i = 0; i < XI; ++i) {
+    for (int i = 0; i < R::kTok; ++i) {
         const int v = min(8 * i + r, 2 * n - 1);
-        src[2 + i] = a.h + ((size_t)(off + (v < n ? v : v - n)) * 2 + (v < n ? 0 : 1)) * a.f + k;
+        src[2 * NM + i] = a.h + ((size_t)(off + (v < n ? v : v - n)) * 2 + (v < n ? 0 : 1)) * a.f + k;
     }
     // this lane's columns: whether hi (0) or lo (1), their router weight and place in y
     int at[R::kFrag], part[R::kFrag];
@@ -341,10 +406,10 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
     for (int j = 0; j < R::kFrag; ++j) {
         const int v = 16 * j + (lane & 15), t = v < n ? v : v - n;
         part[j] = v < n ? 0 : v < 2 * n ? 1 : 2;
-        at[j] = part[j] < 2 ? nth_bit((uint32_t)rec.y, first + t) * 16 + 4 * (lane >> 4) : 0;
+        at[j] = part[j] < 2 ? nth_bit((uint32_t)rec.y, first + t) * 16 * NM + 4 * (lane >> 4) : 0;
         w[j] = part[j] < 2 ? a.tab.wt[off + t] : 0.f;
     }
-    st::stream<BF16, 1, XI, D>(acc, ring, src, b1 - b0, b1 == blocks ? a.f - 64 * (blocks - 1) : 64, lane);
+    st::stream<BF16, NM, XR, D>(acc, ring, src, b1 - b0, b1 == blocks ? a.f - 64 * (blocks - 1) : 64, lane);
     // the hi columns first, then the lo ones: a token's two columns lie in two
     // lanes, whose sums must not be read before the other's are written
 #pragma unroll
@@ -353,43 +418,67 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
         for (int j = 0; j < R::kFrag; ++j)
             if (part[j] == h)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[at[j] + i] += w[j] * acc[0][j][i];
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[at[j] + 16 * m + i] += w[j] * acc[m][j][i];
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
-// XM: groups of 8 hi and lo columns that a pass can have (1, 2 or 4): an expert
-// with more than 16 tokens takes two passes over its weights.  Workgroup b takes
-// columns 16 (b % nblk) .. and part b / nblk of `parts`.
+// XM: hi and lo rows that a pass can have (2, 8, 16 or 32): an expert with more
+// than 16 tokens takes two passes over its weights.  Workgroup b takes columns
+// C (b % nblk) .. and part b / nblk of `parts`; the waves of all parts take
+// equal shares of the blocks' costs, in the order of the list.
 template <bool BF16, int XM>
 __global__ void __launch_bounds__(256)
 few_down_kernel(FewArgs a, int parts)
 {
+    constexpr int NM = kDownM(XM), C = 16 * NM;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int last;
     const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     unsigned char *ring = smem + wave * kDownRing(XM);
-    float *ys = (float *)(smem + waves * kDownRing(XM));    // [waves][T][16]
-    float *y = ys + wave * a.T * 16;
-    for (int i = lane; i < a.T * 16; i += 64) y[i] = 0.f;
-    const int nblk = (a.d + 15) / 16, part = blockIdx.x / nblk, blk = blockIdx.x - part * nblk;
-    const int n0 = 16 * blk;
-    const int n = a.T == 1 ? a.amax : *a.tab.n, blocks = (a.f + 63) / 64;
-    const long long total = (long long)n * blocks, share = part * waves + wave, shares = (long long)parts * waves;
-    const int beg = (int)(total * share / shares), end = (int)(total * (share + 1) / shares);
-    for (int s = beg; s < end;) {
-        const int i = s / blocks, b0 = s - i * blocks, b1 = min(blocks, b0 + end - s);
-        s += b1 - b0;
-        const int4 rec = a.tab.rec[i];
-        const int all = __popc((uint32_t)rec.y);
-        for (int first = 0; first < all; first += 16) {
-            const int m = min(16, all - first);
-            if (XM == 1 || m <= 4)
-                down_wave<BF16, 1, kDownDepth(XM, 1)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
-            else if (XM == 2 || m <= 8)
-                down_wave<BF16, 2, kDownDepth(XM, 2)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
-            else down_wave<BF16, 4, kDownDepth(XM, 4)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
+    float *ys = (float *)(smem + waves * kDownRing(XM));    // [waves][T][C]
+    float *y = ys + wave * a.T * C;
+    for (int i = lane; i < a.T * C; i += 64) y[i] = 0.f;
+    const int nblk = (a.d + C - 1) / C, part = blockIdx.x / nblk, blk = blockIdx.x - part * nblk;
+    const int n0 = C * blk;
+    const int blocks = (a.f + 63) / 64, share = part * waves + wave, shares = parts * waves;
+    if constexpr (XM == 2) {
+        // one token: every listed expert has it
+        const long long total = (long long)a.amax * blocks;
+        const int beg = (int)(total * share / shares), end = (int)(total * (share + 1) / shares);
+        for (int s = beg; s < end;) {
+            const int i = s / blocks, b0 = s - i * blocks, b1 = min(blocks, b0 + end - s);
+            s += b1 - b0;
+            down_wave<BF16, NM, 2, kDownDepth(2, 2)>(a, ring, y, a.tab.rec[i], 0, 1, n0, b0, b1, blocks, lane);
+        }
+    } else {
+        // a list entry's w is the cost of the blocks of one column before it / blocks
+        const int n = *a.tab.n;
+        const long long total = (long long)a.tab.rec[n].w * blocks;
+        const long long beg = total * share / shares, end = total * (share + 1) / shares;
+        int i = -1;                                 // the last entry at or before beg
+        for (int i0 = 0; i0 < n; i0 += 64)
+            i += __popcll(__ballot(i0 + lane < n && (long long)a.tab.rec[i0 + min(lane, n - 1 - i0)].w * blocks <= beg));
+        for (; i < n; ++i) {
+            const int4 rec = a.tab.rec[i];
+            const int all = __popc((uint32_t)rec.y), cost = down_cost(all);
+            const long long at = (long long)rec.w * blocks;
+            if (at >= end) break;
+            // the blocks that begin within the share
+            const int b0 = beg > at ? (int)((beg - at + cost - 1) / cost) : 0;
+            const int b1 = (int)min((long long)blocks, (end - at + cost - 1) / cost);
+            if (b0 >= b1) continue;
+            for (int first = 0; first < all; first += 16) {
+                const int m = min(16, all - first);
+                if (XM == 8 || m <= 4)
+                    down_wave<BF16, NM, 8, kDownDepth(XM, 8)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
+                else if (XM == 16 || m <= 8)
+                    down_wave<BF16, NM, 16, kDownDepth(XM, 16)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
+                else down_wave<BF16, NM, 32, kDownDepth(XM, 32)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
+            }
         }
     }
     __syncthreads();
@@ -398,11 +487,11 @@ few_down_kernel(FewArgs a, int parts)
         if (a.r) v += st::load_el(a.r, a.ydt, at);
         st::store_el(a.y, a.ydt, at, v);
     };
-    for (int q = tid; q < a.T * 16; q += blockDim.x) {
-        const int t = q >> 4, c = n0 + (q & 15);
+    for (int q = tid; q < a.T * C; q += blockDim.x) {
+        const int t = q / C, c = n0 + q % C;
         if (c >= a.d) continue;
         float v = 0.f;
-        for (int z = 0; z < waves; ++z) v += ys[z * a.T * 16 + q];
+        for (int z = 0; z < waves; ++z) v += ys[z * a.T * C + q];
         if (parts == 1) finish(t, c, v);
         else store_coherent(a.part + ((size_t)part * a.T + t) * a.d + c, v);
     }
@@ -419,8 +508,8 @@ few_down_kernel(FewArgs a, int parts)
         last = __hip_atomic_fetch_add(a.tab.done + blk, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
     __syncthreads();
     if (!last) return;
-    for (int q = tid; q < a.T * 16; q += blockDim.x) {
-        const int t = q >> 4, c = n0 + (q & 15);
+    for (int q = tid; q < a.T * C; q += blockDim.x) {
+        const int t = q / C, c = n0 + q % C;
         if (c >= a.d) continue;
         float v = 0.f;
         for (int z = 0; z < parts; ++z) v += load_coherent(a.part + ((size_t)z * a.T + t) * a.d + c);
@@ -443,11 +532,11 @@ hipError_t gateup(const FewArgs &a, hipStream_t s)
     while (P < 8 && units * P < 2048 && blocks >= 8 * P) P *= 2;
     while (P > 1 && blocks < P) P /= 2;
     const int G = P < 4 ? 4 / P : 1, slice = (blocks + P - 1) / P;
-    static_assert(kUpRing(XM) >= (XM + 1) / 2 * 2048, "the sums fit the rings");
+    static_assert(kUpRing(XM) >= (XM + 15) / 16 * 2048, "the sums fit the rings");
     size_t lds = (size_t)G * P * kUpRing(XM);
     const size_t rb = ROUTE == kFromList ? 0 : route_bytes(a.T, a.E, a.k);
     if (rb > lds) lds = rb;
-    if (ROUTE == kFromRouter) lds += 16 * (size_t)a.amax;
+    if (ROUTE == kFromRouter) lds += 16 * (size_t)(a.amax + 1);
     const hipError_t e = allow_lds((const void *)few_gateup_kernel<BF16, XM, ROUTE>, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((few_gateup_kernel<BF16, XM, ROUTE>), dim3((unsigned)((units + G - 1) / G)), dim3(64 * G * P),
@@ -458,23 +547,25 @@ hipError_t gateup(const FewArgs &a, hipStream_t s)
 template <bool BF16>
 hipError_t gateup_for(const FewArgs &a, int route, hipStream_t s)
 {
-    if (a.T <= 8) {
+    if (a.T == 1) {
         if (route == kFromRouter) return gateup<BF16, 1, kFromRouter>(a, s);
         return route == kFromLogits ? gateup<BF16, 1, kFromLogits>(a, s) : gateup<BF16, 1, kFromList>(a, s);
     }
-    return a.T <= 16 ? gateup<BF16, 2, kFromList>(a, s) : gateup<BF16, 4, kFromList>(a, s);
+    if (a.T <= 8) return route == kFromRouter ? gateup<BF16, 8, kFromRouter>(a, s) : gateup<BF16, 8, kFromList>(a, s);
+    return a.T <= 16 ? gateup<BF16, 16, kFromList>(a, s) : gateup<BF16, 32, kFromList>(a, s);
 }
 
 template <bool BF16, int XM>
 hipError_t down(const FewArgs &a, hipStream_t s)
 {
     constexpr int W = 4;
-    const size_t lds = (size_t)W * (kDownRing(XM) + a.T * 64);
+    constexpr int C = 16 * kDownM(XM);
+    const size_t lds = (size_t)W * (kDownRing(XM) + a.T * C * 4);
     const hipError_t e = allow_lds((const void *)few_down_kernel<BF16, XM>, lds);
     if (e != hipSuccess) return e;
     const int parts = few_parts(a.T, a.d, a.f, a.E, a.k, a.S);
-    hipLaunchKernelGGL((few_down_kernel<BF16, XM>), dim3((unsigned)((a.d + 15) / 16 * parts)), dim3(64 * W), lds, s, a,
-                       parts);
+    hipLaunchKernelGGL((few_down_kernel<BF16, XM>), dim3((unsigned)((a.d + C - 1) / C * parts)), dim3(64 * W), lds, s,
+                       a, parts);
     return hipGetLastError();
 }
 
@@ -488,13 +579,14 @@ bool args_ok(const FewArgs &a)
 
 int few_amax(int T, int E, int k, int S) { return (E < T * k ? E : T * k) + S; }
 
-// Workgroups per 16 columns of y: about three per compute unit in all, while
-// each of its 4 waves keeps 4 blocks of 64 channels
+// Workgroups per column block of y (16 columns, 32 from 9 tokens on): about three
+// per compute unit in all, one where their rings fill it, while each of the 4 waves keeps 6
+// blocks of 64 channels
 int few_parts(int T, int d, int f, int E, int k, int S)
 {
-    const int nblk = (d + 15) / 16;
-    const long long most = (long long)few_amax(T, E, k, S) * ((f + 63) / 64) / 16;
-    int p = (768 + nblk - 1) / nblk;
+    const int c = T <= 8 ? 16 : 32, nblk = (d + c - 1) / c, want = T <= 8 ? 768 : 256;
+    const long long most = (long long)few_amax(T, E, k, S) * ((f + 63) / 64) / 24;
+    int p = (want + nblk - 1) / nblk;
     if (p > most) p = most < 1 ? 1 : (int)most;
     if (p > 32) p = 32;
     // one token: shares that start and end with an expert, where a count near p gives them
@@ -517,7 +609,7 @@ hipError_t launch_few(const FewArgs &a, hipStream_t s)
     int route = kFromList;
     if (units <= 1024) {
         if (a.T <= 8 && (long long)a.T * a.E * a.d <= 32768) route = kFromRouter;
-        else if (a.T == 1 && a.E <= 64 * kPick && a.k <= 16) route = kFromLogits;
+        else if (a.T == 1 && a.k <= kSelect) route = kFromLogits;
     }
     hipError_t e = hipSuccess;
     if (route != kFromRouter) {
@@ -539,9 +631,10 @@ hipError_t launch_few(const FewArgs &a, hipStream_t s)
     }
     e = a.bf16 ? gateup_for<true>(a, route, s) : gateup_for<false>(a, route, s);
     if (e != hipSuccess) return e;
-    if (a.T <= 4) return a.bf16 ? down<true, 1>(a, s) : down<false, 1>(a, s);
-    if (a.T <= 8) return a.bf16 ? down<true, 2>(a, s) : down<false, 2>(a, s);
-    return a.bf16 ? down<true, 4>(a, s) : down<false, 4>(a, s);
+    if (a.T == 1) return a.bf16 ? down<true, 2>(a, s) : down<false, 2>(a, s);
+    if (a.T <= 4) return a.bf16 ? down<true, 8>(a, s) : down<false, 8>(a, s);
+    if (a.T <= 8) return a.bf16 ? down<true, 16>(a, s) : down<false, 16>(a, s);
+    return a.bf16 ? down<true, 32>(a, s) : down<false, 32>(a, s);
 }
 
 }  // namespace moeffn

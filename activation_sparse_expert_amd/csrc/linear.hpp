@@ -35,7 +35,7 @@ size_t linear_tile_ws_bytes(int T, int K, int N);       // the larger of the pla
 // last; an expert's tokens have consecutive rows.
 struct FewTab {
     int32_t *n;                         // [1] experts listed
-    int4 *rec;                          // [A] {expert (-1 past the list), token bits, first row, -}
+    int4 *rec;                          // [A + 1] {expert (-1 past the list), token bits, first row, cost before}
     float *wt;                          // [T (k + S)] router weight of each row (shared experts: 1)
     int32_t *done;                      // [ceil(d / 16)] parts of a column block that are written
 };

@@ -13,12 +13,12 @@ namespace {
 using st::floatx4;
 
 // NM: groups of 16 weight rows per wave, the second half of Wg when GATED;
-// XI: groups of 8 tokens; D: blocks in the ring.
-template <bool BF16, bool GATED, int NM, int XI, int D>
+// XR: token rows; D: blocks in the ring.
+template <bool BF16, bool GATED, int NM, int XR, int D>
 __global__ void __launch_bounds__(1024)
 linear_stream_kernel(LinearArgs a, int P, int slice)
 {
-    using R = st::Ring<NM, XI>;
+    using R = st::Ring<NM, XR>;
     constexpr int NB = R::kFrag, NO = GATED ? NM / 2 : NM;      // NO: groups of 16 outputs
     extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -44,8 +44,8 @@ linear_stream_kernel(LinearArgs a, int P, int slice)
             src[i] = (gate ? a.wg : a.w) + (size_t)n * a.K + k;
         }
 #pragma unroll
-        for (int i = 0; i < XI; ++i) src[2 * NM + i] = a.x + (size_t)min(8 * i + r, a.T - 1) * a.xs + k;
-        st::stream<BF16, NM, XI, D>(acc, smem + wave * D * R::kBlock, src, b1 - b0,
+        for (int i = 0; i < R::kTok; ++i) src[2 * NM + i] = a.x + (size_t)min(8 * i + r, a.T - 1) * a.xs + k;
+        st::stream<BF16, NM, XR, D>(acc, smem + wave * D * R::kBlock, src, b1 - b0,
                                     b1 == blocks ? a.K - 64 * (blocks - 1) : 64, lane);
     }
     __syncthreads();                                // the rings are done with
@@ -73,10 +73,10 @@ linear_stream_kernel(LinearArgs a, int P, int slice)
     }
 }
 
-template <bool BF16, bool GATED, int NM, int XI, int D>
+template <bool BF16, bool GATED, int NM, int XR, int D>
 hipError_t launch_one(const LinearArgs &a, hipStream_t s)
 {
-    using R = st::Ring<NM, XI>;
+    using R = st::Ring<NM, XR>;
     constexpr int NO = GATED ? NM / 2 : NM;
     const int units = (a.N + 16 * NO - 1) / (16 * NO), blocks = (a.K + 63) / 64;
     // slices of K: 4, more while the waves are too few to fill the chip and a
@@ -87,35 +87,36 @@ hipError_t launch_one(const LinearArgs &a, hipStream_t s)
     const int G = P < 4 ? 4 / P : 1, slice = (blocks + P - 1) / P;
     constexpr int ring = D * R::kBlock, red = NM * R::kFrag * 1024;
     const int lds = G * P * (ring > red ? ring : red);
-    const void *k = (const void *)linear_stream_kernel<BF16, GATED, NM, XI, D>;
+    const void *k = (const void *)linear_stream_kernel<BF16, GATED, NM, XR, D>;
     if (lds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((linear_stream_kernel<BF16, GATED, NM, XI, D>), dim3((unsigned)((units + G - 1) / G)),
+    hipLaunchKernelGGL((linear_stream_kernel<BF16, GATED, NM, XR, D>), dim3((unsigned)((units + G - 1) / G)),
                        dim3(64 * G * P), lds, s, a, P, slice);
     return hipGetLastError();
 }
 
 // Rows per wave: 16 (and 16 of Wg).  From 17 tokens a block of tokens is larger
 // than that of 16 rows, so wide layers take 32 + 32 or 64.
-template <bool BF16, int XI>
-hipError_t launch_xi(const LinearArgs &a, hipStream_t s)
+template <bool BF16, int XR>
+hipError_t launch_xr(const LinearArgs &a, hipStream_t s)
 {
-    constexpr int D = XI <= 2 ? 4 : 3;
-    if constexpr (XI > 2)
+    if constexpr (XR > 16)
         if (a.N >= 16384)
-            return a.wg ? launch_one<BF16, true, 4, XI, 3>(a, s) : launch_one<BF16, false, 4, XI, 3>(a, s);
-    return a.wg ? launch_one<BF16, true, 2, XI, 3>(a, s) : launch_one<BF16, false, 1, XI, D>(a, s);
+            return a.wg ? launch_one<BF16, true, 4, XR, 3>(a, s) : launch_one<BF16, false, 4, XR, 3>(a, s);
+    constexpr int D = XR <= 16 ? 4 : 3;
+    return a.wg ? launch_one<BF16, true, 2, XR, 3>(a, s) : launch_one<BF16, false, 1, XR, D>(a, s);
 }
 
 template <bool BF16>
 hipError_t launch_t(const LinearArgs &a, hipStream_t s)
 {
-    if (a.T <= 8) return launch_xi<BF16, 1>(a, s);
-    if (a.T <= 16) return launch_xi<BF16, 2>(a, s);
-    if (a.T <= 24) return launch_xi<BF16, 3>(a, s);
-    return launch_xi<BF16, 4>(a, s);
+    if (a.T == 1) return launch_xr<BF16, 1>(a, s);
+    if (a.T <= 8) return launch_xr<BF16, 8>(a, s);
+    if (a.T <= 16) return launch_xr<BF16, 16>(a, s);
+    if (a.T <= 24) return launch_xr<BF16, 24>(a, s);
+    return launch_xr<BF16, 32>(a, s);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
 // Weight-streaming product for a few tokens: one wave multiplies 16 NM weight
-// rows by 8 XI tokens over a run of k,
+// rows by XR tokens over a run of k,
 //   D[row][token] += sum_k W[row][k] X[token][k],
 // with v_mfma_f32_16x16x32: weights as the A operand (lane l holds row l % 16,
 // k 8 (l / 16) .. + 7), tokens as the B operand (lane l: token l % 16, the same
@@ -74,11 +74,15 @@ __device__ __forceinline__ void wait_copies()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <int NM, int XI>
+// XR: token rows of a block (1, 2 or a multiple of 8)
+template <int NM, int XR>
 struct Ring {
-    static constexpr int kCopies = 2 * NM + XI;         // instructions per block
-    static constexpr int kBlock = 1024 * kCopies;       // bytes
-    static constexpr int kFrag = (XI + 1) / 2;          // groups of 16 tokens
+    static constexpr int kTok = (XR + 7) / 8;           // copy instructions of tokens
+    static constexpr int kCopies = 2 * NM + kTok;       // instructions per block
+    static constexpr int kBlock = 2048 * NM + 128 * XR; // bytes
+    static constexpr int kFrag = (XR + 15) / 16;        // groups of 16 tokens
+    typedef floatx4 Acc[NM][kFrag];
+    typedef const uint16_t *Src[kCopies];
 };
 
 // Row r0 = lane / 8 of the 8 rows that a copy instruction fills, and the k
@@ -89,30 +93,28 @@ __device__ __forceinline__ int copy_k(int lane) { return 8 * ((lane & 7) ^ (lane
 
 // nb >= 1 blocks of 64 k, of which the last holds kl (a multiple of 8) values.
 //   src[i]: this lane's source of copy i at the first block (copy_row, copy_k):
-//           2 NM of weights (rows 8 i ..), then XI of tokens
+//           2 NM of weights (rows 8 i ..), then those of the XR token rows
 //   ring:   D blocks of LDS of this wave (wave-uniform)
-// Tokens 8 XI .. of an odd XI repeat the last 8; rows and tokens that do not
-// exist repeat others: their columns and rows of D mean nothing.
-template <bool BF16, int NM, int XI, int D>
-__device__ __forceinline__ void stream(floatx4 (&acc)[NM][(XI + 1) / 2], unsigned char *ring,
-                                       const uint16_t *(&src)[2 * NM + XI], int nb, int kl, int lane)
+// Columns of D past the XR rows repeat some of them; rows and tokens that do not
+// exist may be given as copies of others: their part of D means nothing.
+template <bool BF16, int NM, int XR, int D>
+__device__ __forceinline__ void stream(typename Ring<NM, XR>::Acc &acc, unsigned char *ring,
+                                       typename Ring<NM, XR>::Src &src, int nb, int kl, int lane)
 {
-    using R = Ring<NM, XI>;
+    using R = Ring<NM, XR>;
+    static_assert(XR == 1 || XR == 2 || XR % 8 == 0, "token rows");
     const int li = lane & 15, q = lane >> 4;
     const int kc = copy_k(lane);
     int put = 0, get = 0, issued = 0;
     auto issue = [&]() {
         unsigned char *d = ring + put * R::kBlock;
         put = put + 1 == D ? 0 : put + 1;
-        if (++issued == nb && kl < 64) {
-#pragma unroll
-            for (int i = 0; i < R::kCopies; ++i) copy16_to_lds(kc < kl ? src[i] : zeros16, d + 1024 * i);
-            return;
-        }
+        const bool tail = ++issued == nb && kl < 64;
 #pragma unroll
         for (int i = 0; i < R::kCopies; ++i) {
-            if (i < 2 * NM) copy16_to_lds<true>(src[i], d + 1024 * i);
-            else copy16_to_lds(src[i], d + 1024 * i);
+            const uint16_t *p = tail && kc >= kl ? zeros16 : src[i];
+            if (i < 2 * NM) copy16_to_lds<true>(p, d + 1024 * i);
+            else if (XR >= 8 || lane < 8 * XR) copy16_to_lds(p, d + 1024 * i);
             src[i] += 64;
         }
     };
@@ -121,13 +123,18 @@ __device__ __forceinline__ void stream(floatx4 (&acc)[NM][(XI + 1) / 2], unsigne
         get = get + 1 == D ? 0 : get + 1;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int at = li * 128 + 16 * ((4 * s + q) ^ (li & 7));
+            const int c = 4 * s + q, at = li * 128 + 16 * (c ^ (li & 7));
             uint4 w[NM], x[R::kFrag];
 #pragma unroll
             for (int m = 0; m < NM; ++m) w[m] = *(const uint4 *)(d + 2048 * m + at);
 #pragma unroll
-            for (int j = 0; j < R::kFrag; ++j)
-                x[j] = *(const uint4 *)(d + 2048 * (NM + j) + (2 * j + 1 < XI ? at : at & 1023));
+            for (int j = 0; j < R::kFrag; ++j) {
+                int xt = at;
+                if (XR == 1) xt = 16 * c;
+                else if (XR == 2) xt = (li & 1) * 128 + 16 * (c ^ (li & 1));
+                else if (16 * j + 8 == XR) xt = at & 1023;
+                x[j] = *(const uint4 *)(d + 2048 * (NM + j) + xt);
+            }
 #pragma unroll
             for (int m = 0; m < NM; ++m)
 #pragma unroll

@@ -371,7 +371,7 @@ moe_status moe_layer_forward_few(const moe_layer *L, const void *x, moe_dtype xd
  * MOE_ERR_UNSUPPORTED); x and the weights 16-byte aligned.  The order of the
  * sums depends on T, n and k alone: outputs are bit-reproducible.
  * Workspace: moe_workspace_size(MOE_OP_LINEAR, T, k, n, 0, 0, 0) bytes, gated or
- * not.
+ * not; where that is 0 (up to 32 tokens, and wherever K is not split) ws may be NULL.
  */
 moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt, long long x_stride,
                               int T, const void *residual, long long residual_stride,
@@ -432,7 +432,8 @@ moe_status moe_eamc_match(const int32_t *eamc, int n, int len, const int32_t *qu
                           int32_t *idx_out, double *dist_out,
                           void *ws, size_t ws_bytes, void *stream);
 
-/* Workspace bytes needed by `op` at these sizes (0 when the sizes are invalid). */
+/* Workspace bytes needed by `op` at these sizes (0 when the sizes are invalid;
+ * MOE_OP_LINEAR also where the call needs none). */
 size_t moe_workspace_size(moe_op op, int T, int d, int f, int E, int k, int S);
 
 /* Zero-fill a workspace with a kernel (safe inside stream capture). */

@@ -26,7 +26,8 @@ def _linear(n=704, k=256, wdt=0, w=FAKE, bias=None, w_gate=None, bias_gate=None,
     (dict(x=FAKE + 8), -3), (dict(xs=260), -3), (dict(w=FAKE + 2), -3), (dict(w_gate=FAKE + 8), -3),
     (dict(y=FAKE + 2), -3), (dict(r=FAKE + 2), -3), (dict(bias=FAKE + 2), -3),
     (dict(w_gate=FAKE, bias_gate=FAKE + 1), -3),
-    (dict(ws=None), -4), (dict(ws_bytes=0), -4), (dict(T=40, k=8192, n=64, ws_bytes=256), -4), (dict(ws=FAKE + 4), -3),
+    (dict(T=40, k=8192, n=64, ws=None), -4), (dict(T=40, k=8192, n=64, ws_bytes=0), -4),
+    (dict(T=40, k=8192, n=64, ws_bytes=256), -4), (dict(ws=FAKE + 4), -3),
 ])
 def test_linear_rejects(kw, code):
     assert _linear(**kw) == code
@@ -77,7 +78,7 @@ def test_few_trace_rejects(field, val, code):
 
 def test_workspace_sizes():
     _lib_or_skip()
-    assert moe.workspace_size(moe.OP_LINEAR, 1, 256, 704) > 0
+    assert moe.workspace_size(moe.OP_LINEAR, 1, 256, 704) == 0          # needs none
     assert moe.workspace_size(moe.OP_LINEAR, 1, 260, 704) == 0
     assert moe.workspace_size(moe.OP_LINEAR, 65537, 256, 704) == 0
     # a split of K keeps at least two fp32 products
