@@ -2,12 +2,17 @@
 // k-contiguous, in tiles of BM tokens x BN weight rows staged through LDS (a
 // gated tile holds BN / 2 rows of W and the same outputs' rows of Wg, so that a
 // wave ends with both products of its outputs in registers).  Blocks of 64 k
-// (128-byte rows) are copied global -> LDS by DMA into one stage while the other
-// is multiplied; the 16-byte chunks of a row are XOR-swizzled so that the rows a
-// fragment read serves together fall in distinct banks.
+// (128-byte rows) are copied global -> LDS by DMA while others are multiplied;
+// the 16-byte chunks of a row are XOR-swizzled so that the rows a fragment read
+// serves together fall in distinct banks.  The weights are the matrix
+// instruction's A operand, so that a lane ends with four consecutive outputs of
+// a token and stores them together.
 //
-// With few tiles K is split over workgroups, whose fp32 products a second kernel
-// adds in a fixed order before the epilogue.
+// Two kernels.  Large products take 256 x 256 tiles and 8 waves in two groups
+// half a step apart (linear_big_kernel).  The others take smaller tiles with
+// several blocks in flight (linear_tile_kernel); where those are few, K is split
+// over workgroups, whose fp32 products a second kernel adds in a fixed order
+// before the epilogue.
 #include "linear_epilogue.hpp"
 
 namespace moeffn {
@@ -32,12 +37,102 @@ __device__ __forceinline__ floatx16 mma32(const uint4 &a, const uint4 &b, const 
 __device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 __device__ __forceinline__ int lds_at(int row, int c) { return row * 128 + 16 * (c ^ swizzle(row)); }
 
-// How a call is cut: tiles of outputs, and K in `split` runs of `blocks` blocks.
+// How a call is cut: tiles of outputs, K in `split` runs of `blocks` blocks, and
+// whether the epilogue goes by fours.
 struct Cut {
-    int tm, tn, split, blocks;
+    int tm, tn, split, blocks, quads;
 };
 
-template <bool BF16, int BM, int BN, int WM, int WN, bool GATED>
+// The tile of workgroup b, which runs on XCD b % 8: each XCD takes a contiguous
+// run of the tile order, in which groups of 4 token tiles pass over the outputs
+// together, so that the tiles resident on an XCD share operands in its L2.
+struct Place {
+    int t, n, ks;                                   // tile of tokens and of outputs, run of K
+    bool none;
+};
+__device__ __forceinline__ Place place(const Cut &c)
+{
+    constexpr int GM = 4;
+    const int tiles = c.tm * c.tn * c.split, q8 = (tiles + 7) / 8;
+    const int idx = (blockIdx.x & 7) * q8 + (blockIdx.x >> 3);
+    Place p{};
+    p.none = (int)(blockIdx.x >> 3) >= q8 || idx >= tiles;
+    p.ks = idx / (c.tm * c.tn);
+    const int id = idx - p.ks * c.tm * c.tn;
+    const int grp = id / (GM * c.tn), gm = min(GM, c.tm - grp * GM), in = id - grp * GM * c.tn;
+    p.t = grp * GM + in % gm;
+    p.n = in / gm;
+    return p;
+}
+
+// This lane's source (at k = 0) of 8 rows that a copy instruction fills: lane l
+// row l / 8, chunk l % 8 as stored.  Rows past the last token or output repeat it.
+template <int ON, int BM, bool GATED>
+__device__ __forceinline__ const uint16_t *row_source(const LinearArgs &a, int t0, int n0, int row, int lane)
+{
+    const int k = 8 * ((lane & 7) ^ swizzle(row));
+    if (row < BM) return a.x + (size_t)min(t0 + row, a.T - 1) * a.xs + k;
+    const int br = row - BM;
+    const bool gate = GATED && br >= ON;
+    return (gate ? a.wg : a.w) + (size_t)min(n0 + (gate ? br - ON : br), a.N - 1) * a.K + k;
+}
+
+// Epilogue of a wave's subtiles (value r of lane l of a subtile is output
+// 8 (r / 4) + 4 (l / 32) + r % 4, token l % 32): 32 tokens at a time through LDS
+// of the wave's own, so that it stores whole runs of a token's outputs.
+constexpr int kPadRow(int tn) { return 32 * tn + 4; }
+constexpr int kWaveLds(int tn) { return 32 * kPadRow(tn) * 4; }
+
+template <int TM, int TN, bool GATED>
+__device__ __forceinline__ void store_tile(const LinearArgs &a, const Cut &c, int ks, int t0, int n0, int lane,
+                                           float *lds, const floatx16 (&acc)[TM][TN])
+{
+    constexpr int HN = GATED ? TN / 2 : TN, LD = kPadRow(TN);
+    const size_t plane = (size_t)a.T * a.N;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *(float4 *)&lds[(lane & 31) * LD + 32 * j + 8 * q + 4 * (lane >> 5)] =
+                    make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // written by other lanes of this wave
+#pragma unroll 1
+        for (int e = lane; e < 32 * 8 * HN; e += 64) {
+            const int t = e / (8 * HN), col = 4 * (e % (8 * HN)), n = n0 + col;
+            const float4 v4 = *(const float4 *)&lds[t * LD + col];
+            const float4 g4 = *(const float4 *)&lds[t * LD + col + (GATED ? 32 * HN : 0)];
+            const float v[4] = {v4.x, v4.y, v4.z, v4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w};
+            const int tok = t0 + 32 * i + t;
+            if (tok >= a.T || n >= a.N) continue;
+            if (c.split > 1) {
+                float *p = a.part + (size_t)ks * (GATED ? 2 : 1) * plane + (size_t)tok * a.N + n;
+                if (c.quads) {
+                    *(float4 *)p = v4;
+                    if (GATED) *(float4 *)(p + plane) = g4;
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (n + x < a.N) {
+                            p[x] = v[x];
+                            if (GATED) p[plane + x] = g[x];
+                        }
+                }
+            } else if (c.quads) {
+                le::finish4(a, tok, n, v, g);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (n + x < a.N) le::finish(a, tok, n + x, v[x], g[x]);
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // read before the next 32 tokens are written
+    }
+}
+
+// S stages: blocks kb + 1 .. kb + S - 1 are in flight while block kb is multiplied.
+template <bool BF16, int BM, int BN, int WM, int WN, bool GATED, int S>
 __global__ void __launch_bounds__(64 * WM * WN)
 linear_tile_kernel(LinearArgs a, Cut c)
 {
@@ -45,53 +140,35 @@ linear_tile_kernel(LinearArgs a, Cut c)
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32, HN = GATED ? TN / 2 : TN;
     constexpr int kStage = (BM + BN) * 128, NI = (BM + BN) / 8 / W;
     static_assert((BM + BN) % (8 * W) == 0 && (!GATED || TN % 2 == 0), "tile");
-    extern __shared__ __align__(16) unsigned char smem[];   // [2][kStage]
+    extern __shared__ __align__(16) unsigned char smem[];   // [S][kStage]
+    const Place at = place(c);
+    if (at.none) return;
+    const int t0 = at.t * BM, n0 = at.n * ON;
 
-    // Workgroup b runs on XCD b % 8: each XCD takes a contiguous run of the tile
-    // order, in which groups of 4 token tiles pass over the outputs together, so
-    // that the tiles resident on an XCD share operands in its L2.
-    const int tiles = c.tm * c.tn * c.split, q8 = (tiles + 7) / 8;
-    const int idx = (blockIdx.x & 7) * q8 + (blockIdx.x >> 3);
-    if (idx >= tiles) return;
-    const int ks = idx / (c.tm * c.tn), id = idx - ks * c.tm * c.tn;
-    constexpr int GM = 4;
-    const int grp = id / (GM * c.tn), gm = min(GM, c.tm - grp * GM);
-    const int in = id - grp * GM * c.tn;
-    const int t0 = (grp * GM + in % gm) * BM, n0 = in / gm * ON;
-
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;
-    const int kb0 = ks * c.blocks, kb1 = min(kb0 + c.blocks, (a.K + kKB - 1) / kKB);
+    const int kb0 = at.ks * c.blocks, kb1 = min(kb0 + c.blocks, (a.K + kKB - 1) / kKB);
 
-    // copy sources: instruction q of this wave fills 8 rows of the stage, lane l
-    // row l / 8, chunk l % 8 as stored; rows past the last token or output repeat it
     const uint16_t *src[NI];
-    int ch[NI];
+    int ck[NI];
 #pragma unroll
     for (int q = 0; q < NI; ++q) {
         const int row = 8 * (wave + W * q) + (lane >> 3);
-        ch[q] = 8 * ((lane & 7) ^ swizzle(row));
-        if (row < BM) {
-            src[q] = a.x + (size_t)min(t0 + row, a.T - 1) * a.xs + ch[q];
-        } else {
-            const int br = row - BM;
-            const bool gate = GATED && br >= BN / 2;
-            const int n = min(n0 + (gate ? br - BN / 2 : br), a.N - 1);
-            src[q] = (gate ? a.wg : a.w) + (size_t)n * a.K + ch[q];
-        }
+        src[q] = row_source<ON, BM, GATED>(a, t0, n0, row, lane) + (size_t)kb0 * kKB;
+        ck[q] = 8 * ((lane & 7) ^ swizzle(row));
     }
-    auto issue = [&](int kb, int stage) {
-        unsigned char *base = smem + stage * kStage;
-        if ((kb + 1) * kKB <= a.K) {
+    int put = 0, next = kb0;
+    auto issue = [&]() {
+        unsigned char *base = smem + put * kStage;
+        put = put + 1 == S ? 0 : put + 1;
+        const bool tail = (next + 1) * kKB > a.K;
 #pragma unroll
-            for (int q = 0; q < NI; ++q)
-                copy16_to_lds(src[q] + (size_t)kb * kKB, base + 1024 * (wave + W * q));
-        } else {
-#pragma unroll
-            for (int q = 0; q < NI; ++q)
-                copy16_to_lds(kb * kKB + ch[q] < a.K ? src[q] + (size_t)kb * kKB : st::zeros16,
-                              base + 1024 * (wave + W * q));
+        for (int q = 0; q < NI; ++q) {
+            copy16_to_lds(tail && next * kKB + ck[q] >= a.K ? st::zeros16 : src[q], base + 1024 * (wave + W * q));
+            src[q] += kKB;
         }
+        ++next;
     };
 
     floatx16 acc[TM][TN];
@@ -108,14 +185,20 @@ linear_tile_kernel(LinearArgs a, Cut c)
     for (int i = 0; i < TM; ++i) arow[i] = BM / WM * wm + 32 * i + li;
 #pragma unroll
     for (int j = 0; j < TN; ++j)
-        brow[j] = BM + (j < HN ? 32 * HN * wn + 32 * j : BN / 2 + 32 * HN * wn + 32 * (j - HN)) + li;
+        brow[j] = BM + (j < HN ? 32 * HN * wn + 32 * j : ON + 32 * HN * wn + 32 * (j - HN)) + li;
 
-    issue(kb0, 0);
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s)
+        if (next < kb1) issue();
+    int get = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();                            // block kb has landed; the other stage is free
-        if (kb + 1 < kb1) issue(kb + 1, (kb + 1 - kb0) & 1);
-        const unsigned char *stg = smem + ((kb - kb0) & 1) * kStage;
+        // block kb has landed, and every wave is done with block kb - 1, whose stage is filled next
+        if (next - kb >= S - 1) st::wait_copies<NI * (S - 2)>();
+        else st::wait_copies<0>();
+        __syncthreads();
+        if (next < kb1) issue();
+        const unsigned char *stg = smem + get * kStage;
+        get = get + 1 == S ? 0 : get + 1;
 #pragma unroll
         for (int s = 0; s < kKB / 16; ++s) {
             uint4 av[TM], bv[TN];
@@ -126,32 +209,135 @@ linear_tile_kernel(LinearArgs a, Cut c)
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mma32<BF16>(av[i], bv[j], acc[i][j]);
+                for (int j = 0; j < TN; ++j) acc[i][j] = mma32<BF16>(bv[j], av[i], acc[i][j]);
         }
     }
+    __syncthreads();                                // the stages are done with
+    static_assert(W * kWaveLds(TN) <= S * kStage, "the epilogue fits the stages");
+    store_tile<TM, TN, GATED>(a, c, at.ks, t0 + BM / WM * wm, n0 + 32 * HN * wn, lane,
+                              (float *)(smem + wave * kWaveLds(TN)), acc);
+}
 
-    // value r of lane l of a subtile: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
-    const size_t plane = (size_t)a.T * a.N;
+// 256 x 256 tiles, 8 waves of 128 tokens x 64 weight rows each (4 x 2 subtiles).
+// A block of 64 k takes a wave four phases, a barrier of the workgroup after each:
+//   L0  reads the fragments of its weight rows and of its first 64 tokens,
+//   M0  multiplies them (16 MFMAs, 512 cycles),
+//   L1  reads those of its other 64 tokens,   M1  multiplies.
+// Waves 4-7 run one phase behind waves 0-3, and every SIMD holds one of each:
+// while one group multiplies the other reads LDS, which at 256 KB a block (192 read, 64
+// written) would bound this tile by itself if the two did not overlap.
+// The parts of a stage are refilled as soon as both groups have read them: the
+// weights and first tokens of block kb + 2 in L1 of block kb, the other tokens
+// of block kb + 1 in L0, so two stages keep 4 phases between a copy and the wait for it.
+template <bool BF16, bool GATED>
+__global__ void __launch_bounds__(512, 2)
+linear_big_kernel(LinearArgs a, Cut c)
+{
+    constexpr int ON = GATED ? 128 : 256, HN = GATED ? 1 : 2;
+    constexpr int kStage = 512 * 128;
+    extern __shared__ __align__(16) unsigned char smem[];   // [2][256 token rows, 256 weight rows][128 B]
+    const Place at = place(c);
+    if (at.none) return;
+    const int t0 = at.t * 256, n0 = at.n * ON;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int nkb = (a.K + kKB - 1) / kKB;
+
+    // copies of this wave: 4 of weight rows, 2 of the first 64 tokens of either
+    // half, 2 of the others
+    const uint16_t *src[8];
+    int dst[8], ck[8];
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int q = 0; q < 8; ++q) {
+        int row = q < 4 ? 256 + 8 * (wave + 8 * q) : 8 * (wave + 8 * (q & 1));   // row of 128 for tokens
+        if (q >= 4) row = (row & 63) + 128 * (row >> 6) + (q >= 6 ? 64 : 0);
+        dst[q] = row * 128;
+        row += lane >> 3;
+        src[q] = row_source<ON, 256, GATED>(a, t0, n0, row, lane);
+        ck[q] = 8 * ((lane & 7) ^ swizzle(row));
+    }
+    // past the last block the copies read zeros (nobody reads them), so that the number in flight stays the same
+    auto copy = [&](int q, int kb) {
+        const int k = kb * kKB + ck[q];
+        copy16_to_lds(k < a.K ? src[q] + (size_t)kb * kKB : st::zeros16, smem + (kb & 1) * kStage + dst[q]);
+    };
+    auto copy_first = [&](int kb) {
 #pragma unroll
-        for (int j = 0; j < HN; ++j) {
-            const int n = n0 + 32 * HN * wn + 32 * j + li;
-            if (n >= a.N) continue;
+        for (int q = 0; q < 6; ++q) copy(q, kb);
+    };
+    auto copy_rest = [&](int kb) {
+        copy(6, kb);
+        copy(7, kb);
+    };
+
+    floatx16 acc[4][2];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int t = t0 + BM / WM * wm + 32 * i + 8 * (r >> 2) + 4 * hk + (r & 3);
-                if (t >= a.T) continue;
-                const float g = GATED ? acc[i][GATED ? j + HN : j][r] : 0.f;
-                if (c.split > 1) {
-                    float *p = a.part + (size_t)ks * (GATED ? 2 : 1) * plane + (size_t)t * a.N + n;
-                    p[0] = acc[i][j][r];
-                    if (GATED) p[plane] = g;
-                } else {
-                    le::finish(a, t, n, acc[i][j][r], g);
-                }
-            }
-        }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    const int li = lane & 31, hk = lane >> 5;
+    int brow[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) brow[j] = 256 + (GATED ? 128 * j + 32 * wn : 64 * wn + 32 * j) + li;
+
+    uint4 av[2][4], bv[2][4];
+    auto read_a = [&](const unsigned char *stg, int half) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                av[i][s] = *(const uint4 *)(stg + lds_at(128 * wm + 64 * half + 32 * i + li, 2 * s + hk));
+    };
+    auto read_b = [&](const unsigned char *stg) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) bv[j][s] = *(const uint4 *)(stg + lds_at(brow[j], 2 * s + hk));
+    };
+    // end of a reading phase: the reads are done, and all but this wave's last 8 copies
+    auto end_read = []() {
+        asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto multiply = [&](int half) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[2 * half + i][j] = mma32<BF16>(bv[j][s], av[i][s], acc[2 * half + i][j]);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    copy_first(0);
+    copy_rest(0);
+    copy_first(1);
+    asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
+    if (wm == 1) asm volatile("s_barrier" ::: "memory");
+    for (int kb = 0; kb < nkb; ++kb) {
+        const unsigned char *stg = smem + (kb & 1) * kStage;
+        read_b(stg);
+        read_a(stg, 0);
+        copy_rest(kb + 1);
+        end_read();
+        multiply(0);
+        read_a(stg, 1);
+        copy_first(kb + 2);
+        end_read();
+        multiply(1);
+    }
+    if (wm == 0) asm volatile("s_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // the copies past the last block too
+    __syncthreads();
+    store_tile<4, 2, GATED>(a, c, 0, t0 + 128 * wm, n0 + 32 * HN * wn, lane, (float *)(smem + wave * kWaveLds(2)), acc);
 }
 
 // Sum of the split's products, in order, and the epilogue.
@@ -169,10 +355,10 @@ linear_join_kernel(LinearArgs a, int split)
     le::finish(a, t, n, v[0], v[1]);
 }
 
-// Tile sizes by the number of tiles they give: 128 tokens x 128 weight rows, or
-// 64 x 64 outputs while those leave compute units idle.
+// Tile sizes by the number of tiles they give: 256 x 256 weight rows, 128 x
+// 128, or 64 x 64 outputs while those leave compute units idle.
 struct Plan {
-    int bm;                                         // 128 or 64
+    int bm;                                         // 256, 128 or 64
     Cut c;
 };
 
@@ -181,38 +367,48 @@ constexpr int kMaxSplit = 8;
 Plan plan(int T, int K, int N, bool gated)
 {
     const int nkb = (K + kKB - 1) / kKB;
-    Plan p;
-    const long long big = (long long)((T + 127) / 128) * ((N + (gated ? 63 : 127)) / (gated ? 64 : 128));
-    p.bm = big >= 256 ? 128 : 64;
-    const int on = p.bm == 128 && !gated ? 128 : 64;
+    auto tiles = [&](int m, int n) { return (long long)((T + m - 1) / m) * ((N + n - 1) / n); };
+    const int g = gated ? 2 : 1;
+    Plan p{};
+    p.bm = tiles(256, 256 / g) >= 192 ? 256 : tiles(128, 128 / g) >= 256 ? 128 : 64;
+    const int on = p.bm == 64 ? 64 : p.bm / g;
     p.c.tm = (T + p.bm - 1) / p.bm;
     p.c.tn = (N + on - 1) / on;
     int split = 1;
-    while (split < kMaxSplit && (long long)p.c.tm * p.c.tn * split < 256 && nkb >= 16 * split) split *= 2;
+    if (p.bm == 64)
+        while (split < kMaxSplit && (long long)p.c.tm * p.c.tn * split < 256 && nkb >= 16 * split) split *= 2;
     p.c.blocks = (nkb + split - 1) / split;
     p.c.split = (nkb + p.c.blocks - 1) / p.c.blocks;
     return p;
 }
 
-template <bool BF16, int BM, int BN, int WM, int WN, bool GATED>
-hipError_t launch_one(const LinearArgs &a, const Cut &c, hipStream_t s)
+hipError_t launch_cut(const void *k, const LinearArgs &a, const Cut &c, int threads, int lds, hipStream_t s)
 {
-    constexpr int lds = 2 * (BM + BN) * 128;
-    const void *k = (const void *)linear_tile_kernel<BF16, BM, BN, WM, WN, GATED>;
-    hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (e != hipSuccess) return e;
+    if (lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    void *args[] = {(void *)&a, (void *)&c};
     const unsigned grid = (unsigned)((c.tm * c.tn * c.split + 7) / 8 * 8);
-    hipLaunchKernelGGL((linear_tile_kernel<BF16, BM, BN, WM, WN, GATED>), dim3(grid), dim3(64 * WM * WN), lds, s, a, c);
-    return hipGetLastError();
+    const hipError_t e = hipLaunchKernel(k, dim3(grid), dim3(threads), args, lds, s);
+    return e != hipSuccess ? e : hipGetLastError();
+}
+
+template <bool BF16, int BM, int BN, bool GATED, int S>
+hipError_t launch_tile(const LinearArgs &a, const Cut &c, hipStream_t s)
+{
+    return launch_cut((const void *)linear_tile_kernel<BF16, BM, BN, 2, 2, GATED, S>, a, c, 256, S * (BM + BN) * 128, s);
 }
 
 template <bool BF16>
 hipError_t launch_t(const LinearArgs &a, const Plan &p, hipStream_t s)
 {
+    if (p.bm == 256)
+        return launch_cut(a.wg ? (const void *)linear_big_kernel<BF16, true> : (const void *)linear_big_kernel<BF16, false>,
+                          a, p.c, 512, 2 * 512 * 128, s);
     if (p.bm == 128)
-        return a.wg ? launch_one<BF16, 128, 128, 2, 2, true>(a, p.c, s)
-                    : launch_one<BF16, 128, 128, 2, 2, false>(a, p.c, s);
-    return a.wg ? launch_one<BF16, 64, 128, 2, 2, true>(a, p.c, s) : launch_one<BF16, 64, 64, 2, 2, false>(a, p.c, s);
+        return a.wg ? launch_tile<BF16, 128, 128, true, 2>(a, p.c, s) : launch_tile<BF16, 128, 128, false, 2>(a, p.c, s);
+    return a.wg ? launch_tile<BF16, 64, 128, true, 3>(a, p.c, s) : launch_tile<BF16, 64, 64, false, 4>(a, p.c, s);
 }
 
 }  // namespace
@@ -227,7 +423,8 @@ size_t linear_tile_ws_bytes(int T, int K, int N)
 hipError_t launch_linear_tile(const LinearArgs &a, hipStream_t s)
 {
     if (a.T < 1 || a.K < 8 || a.K % 8 != 0 || a.N < 1) return hipErrorInvalidValue;
-    const Plan p = plan(a.T, a.K, a.N, a.wg != nullptr);
+    Plan p = plan(a.T, a.K, a.N, a.wg != nullptr);
+    p.c.quads = p.c.split > 1 ? a.N % 4 == 0 : le::quads(a);
     const hipError_t e = a.bf16 ? launch_t<true>(a, p, s) : launch_t<false>(a, p, s);
     if (e != hipSuccess || p.c.split == 1) return e;
     hipLaunchKernelGGL(linear_join_kernel, dim3((unsigned)((a.N + 255) / 256), (unsigned)a.T), dim3(256), 0, s, a,
