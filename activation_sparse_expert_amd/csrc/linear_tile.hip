@@ -103,7 +103,7 @@ __device__ __forceinline__ void store_tile(const LinearArgs &a, const Cut &c, in
             const int t = e / (8 * HN), col = 4 * (e % (8 * HN)), n = n0 + col;
             const float4 v4 = *(const float4 *)&lds[t * LD + col];
             const float4 g4 = *(const float4 *)&lds[t * LD + col + (GATED ? 32 * HN : 0)];
-            const float v[4] = {v4.x, v4.y, v4.z, v4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w};
+            float v[4] = {v4.x, v4.y, v4.z, v4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w};
             const int tok = t0 + 32 * i + t;
             if (tok >= a.T || n >= a.N) continue;
             if (c.split > 1) {
@@ -218,17 +218,27 @@ linear_tile_kernel(LinearArgs a, Cut c)
                               (float *)(smem + wave * kWaveLds(TN)), acc);
 }
 
+// copy16_to_lds with the source as a scalar base and a 32-bit byte offset per
+// lane, so that a block costs no vector arithmetic.
+__device__ __forceinline__ void copy16_to_lds_at(const void *base, uint32_t off, void *lds_base)
+{
+    typedef __attribute__((address_space(3))) void lvoid;
+    const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lvoid *)lds_base);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(m)
+                 : "m0", "memory");
+}
+
 // 256 x 256 tiles, 8 waves of 128 tokens x 64 weight rows each (4 x 2 subtiles).
-// A block of 64 k takes a wave four phases, a barrier of the workgroup after each:
-//   L0  reads the fragments of its weight rows and of its first 64 tokens,
-//   M0  multiplies them (16 MFMAs, 512 cycles),
-//   L1  reads those of its other 64 tokens,   M1  multiplies.
-// Waves 4-7 run one phase behind waves 0-3, and every SIMD holds one of each:
-// while one group multiplies the other reads LDS, which at 256 KB a block (192 read, 64
-// written) would bound this tile by itself if the two did not overlap.
-// The parts of a stage are refilled as soon as both groups have read them: the
-// weights and first tokens of block kb + 2 in L1 of block kb, the other tokens
-// of block kb + 1 in L0, so two stages keep 4 phases between a copy and the wait for it.
+// A block of 64 k takes a wave two phases, a barrier of the workgroup after each:
+// it reads its 24 fragments, then multiplies them (32 MFMAs, 1024 cycles).
+// Waves 4-7 run one phase behind waves 0-3 and every SIMD holds one of each, so
+// that while one group multiplies the other reads LDS: 192 KB a block, with 64 KB
+// written, which is all that LDS moves in the time of the MFMAs and would bound the
+// tile by itself if the two did not overlap.  (Four phases of 16 MFMAs, whose
+// barriers and first reads each cost about 270 cycles, took 3100 cycles a block.)
+// The copies of block kb + 1 are issued when both groups have read block kb - 1,
+// two phases before they are needed.
 template <bool BF16, bool GATED>
 __global__ void __launch_bounds__(512, 2)
 linear_big_kernel(LinearArgs a, Cut c)
@@ -244,31 +254,41 @@ linear_big_kernel(LinearArgs a, Cut c)
     const int wm = wave >> 2, wn = wave & 3;
     const int nkb = (a.K + kKB - 1) / kKB;
 
-    // copies of this wave: 4 of weight rows, 2 of the first 64 tokens of either
-    // half, 2 of the others
-    const uint16_t *src[8];
-    int dst[8], ck[8];
+    // copies 0-3 of this wave fill token rows 8 (wave + 8 q) .., 4-7 weight rows;
+    // sources as byte offsets from the tile's first row (launch_linear_tile sees to it
+    // that they fit)
+    const uint16_t *xb = a.x + (size_t)t0 * a.xs;
+    const uint16_t *wb[2] = {a.w + (size_t)n0 * a.K, (GATED ? a.wg : a.w) + (size_t)n0 * a.K};
+    uint32_t off[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-        int row = q < 4 ? 256 + 8 * (wave + 8 * q) : 8 * (wave + 8 * (q & 1));   // row of 128 for tokens
-        if (q >= 4) row = (row & 63) + 128 * (row >> 6) + (q >= 6 ? 64 : 0);
-        dst[q] = row * 128;
-        row += lane >> 3;
-        src[q] = row_source<ON, 256, GATED>(a, t0, n0, row, lane);
-        ck[q] = 8 * ((lane & 7) ^ swizzle(row));
+        const int row = 8 * (wave + 8 * (q & 3)) + (lane >> 3);
+        const int k = 8 * ((lane & 7) ^ swizzle(row));
+        if (q < 4) off[q] = 2u * (uint32_t)(min(row, a.T - 1 - t0) * a.xs + k);
+        else off[q] = 2u * (uint32_t)(min(GATED ? row & 127 : row, a.N - 1 - n0) * a.K + k);
     }
-    // past the last block the copies read zeros (nobody reads them), so that the number in flight stays the same
-    auto copy = [&](int q, int kb) {
-        const int k = kb * kKB + ck[q];
-        copy16_to_lds(k < a.K ? src[q] + (size_t)kb * kKB : st::zeros16, smem + (kb & 1) * kStage + dst[q]);
-    };
-    auto copy_first = [&](int kb) {
+    // In a last block that K does not fill, lanes past K copy the row's last 8
+    // values; once landed, zero_tail puts zeros in their place.
+    const int left = a.K - (nkb - 1) * kKB;         // k values of the last block
+    auto past = [&](int q) { return 8 * ((lane & 7) ^ swizzle(8 * (wave + 8 * (q & 3)) + (lane >> 3))) - (left - 8); };
+    auto copy_block = [&](int kb) {
+        unsigned char *st = smem + (kb & 1) * kStage + 1024 * wave;
+        const bool tail = kb == nkb - 1 && left < kKB;
 #pragma unroll
-        for (int q = 0; q < 6; ++q) copy(q, kb);
+        for (int q = 0; q < 8; ++q) {
+            const uint16_t *b = q < 4 ? xb : wb[GATED && q >= 6 ? 1 : 0];
+            uint32_t o = off[q];
+            if (tail) o -= 2u * (uint32_t)max(past(q), 0);
+            copy16_to_lds_at(b + (size_t)kb * kKB, o, st + 8192 * q);
+        }
     };
-    auto copy_rest = [&](int kb) {
-        copy(6, kb);
-        copy(7, kb);
+    auto zero_tail = [&](int kb) {
+        if (kb != nkb - 1 || left == kKB) return;
+        unsigned char *st = smem + (kb & 1) * kStage + 1024 * wave + 16 * lane;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (past(q) > 0) *(uint4 *)(st + 8192 * q) = make_uint4(0, 0, 0, 0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     };
 
     floatx16 acc[4][2];
@@ -283,59 +303,61 @@ linear_big_kernel(LinearArgs a, Cut c)
 #pragma unroll
     for (int j = 0; j < 2; ++j) brow[j] = 256 + (GATED ? 128 * j + 32 * wn : 64 * wn + 32 * j) + li;
 
-    uint4 av[2][4], bv[2][4];
-    auto read_a = [&](const unsigned char *stg, int half) {
+    uint4 av[4][4], bv[2][4];
+    auto read_block = [&](int kb) {
+        const unsigned char *st = smem + (kb & 1) * kStage;
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 4; ++s) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                av[i][s] = *(const uint4 *)(stg + lds_at(128 * wm + 64 * half + 32 * i + li, 2 * s + hk));
+            for (int j = 0; j < 2; ++j) bv[j][s] = *(const uint4 *)(st + lds_at(brow[j], 2 * s + hk));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) av[i][s] = *(const uint4 *)(st + lds_at(128 * wm + 32 * i + li, 2 * s + hk));
+        }
     };
-    auto read_b = [&](const unsigned char *stg) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) bv[j][s] = *(const uint4 *)(stg + lds_at(brow[j], 2 * s + hk));
-    };
-    // end of a reading phase: the reads are done, and all but this wave's last 8 copies
-    auto end_read = []() {
-        asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    auto multiply = [&]() {
         __builtin_amdgcn_sched_barrier(0);
-    };
-    auto multiply = [&](int half) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[2 * half + i][j] = mma32<BF16>(bv[j][s], av[i][s], acc[2 * half + i][j]);
+                for (int j = 0; j < 2; ++j) acc[i][j] = mma32<BF16>(bv[j][s], av[i][s], acc[i][j]);
         __builtin_amdgcn_s_setprio(0);
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    copy_first(0);
-    copy_rest(0);
-    copy_first(1);
-    asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
-    if (wm == 1) asm volatile("s_barrier" ::: "memory");
-    for (int kb = 0; kb < nkb; ++kb) {
-        const unsigned char *stg = smem + (kb & 1) * kStage;
-        read_b(stg);
-        read_a(stg, 0);
-        copy_rest(kb + 1);
-        end_read();
-        multiply(0);
-        read_a(stg, 1);
-        copy_first(kb + 2);
-        end_read();
-        multiply(1);
+    copy_block(0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    zero_tail(0);
+    asm volatile("s_barrier" ::: "memory");
+    // phase p of the workgroup: waves 0-3 read block p / 2 or multiply it, waves
+    // 4-7 do what those did in phase p - 1; both copy in even phases and have
+    // their copies waited for by the end of the odd ones
+    if (wm == 0) {
+        for (int kb = 0; kb < nkb; ++kb) {
+            read_block(kb);
+            if (kb + 1 < nkb) copy_block(kb + 1);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            multiply();
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            zero_tail(kb + 1);
+            asm volatile("s_barrier" ::: "memory");
+        }
+        asm volatile("s_barrier" ::: "memory");
+    } else {
+        if (nkb > 1) copy_block(1);
+        asm volatile("s_barrier" ::: "memory");
+        for (int kb = 0; kb < nkb; ++kb) {
+            read_block(kb);
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            zero_tail(kb + 1);
+            asm volatile("s_barrier" ::: "memory");
+            if (kb + 2 < nkb) copy_block(kb + 2);
+            multiply();
+            asm volatile("s_barrier" ::: "memory");
+        }
     }
-    if (wm == 0) asm volatile("s_barrier" ::: "memory");
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // the copies past the last block too
     __syncthreads();
     store_tile<4, 2, GATED>(a, c, 0, t0 + 128 * wm, n0 + 32 * HN * wn, lane, (float *)(smem + wave * kWaveLds(2)), acc);
 }
@@ -364,13 +386,14 @@ struct Plan {
 
 constexpr int kMaxSplit = 8;
 
-Plan plan(int T, int K, int N, bool gated)
+// big_ok: the offsets of a 256-row tile fit 32 bits (linear_big_kernel)
+Plan plan(int T, int K, int N, bool gated, bool big_ok)
 {
     const int nkb = (K + kKB - 1) / kKB;
     auto tiles = [&](int m, int n) { return (long long)((T + m - 1) / m) * ((N + n - 1) / n); };
     const int g = gated ? 2 : 1;
     Plan p{};
-    p.bm = tiles(256, 256 / g) >= 192 ? 256 : tiles(128, 128 / g) >= 256 ? 128 : 64;
+    p.bm = big_ok && tiles(256, 256 / g) >= 192 ? 256 : tiles(128, 128 / g) >= 256 ? 128 : 64;
     const int on = p.bm == 64 ? 64 : p.bm / g;
     p.c.tm = (T + p.bm - 1) / p.bm;
     p.c.tn = (N + on - 1) / on;
@@ -415,7 +438,7 @@ hipError_t launch_t(const LinearArgs &a, const Plan &p, hipStream_t s)
 
 size_t linear_tile_ws_bytes(int T, int K, int N)
 {
-    const Plan p = plan(T, K, N, false), g = plan(T, K, N, true);
+    const Plan p = plan(T, K, N, false, true), g = plan(T, K, N, true, true);
     const size_t np = p.c.split > 1 ? p.c.split : 0, ng = g.c.split > 1 ? 2 * g.c.split : 0;
     return (np > ng ? np : ng) * (size_t)T * N * 4;
 }
@@ -423,7 +446,7 @@ size_t linear_tile_ws_bytes(int T, int K, int N)
 hipError_t launch_linear_tile(const LinearArgs &a, hipStream_t s)
 {
     if (a.T < 1 || a.K < 8 || a.K % 8 != 0 || a.N < 1) return hipErrorInvalidValue;
-    Plan p = plan(a.T, a.K, a.N, a.wg != nullptr);
+    Plan p = plan(a.T, a.K, a.N, a.wg != nullptr, a.xs <= (1 << 21));
     p.c.quads = p.c.split > 1 ? a.N % 4 == 0 : le::quads(a);
     const hipError_t e = a.bf16 ? launch_t<true>(a, p, s) : launch_t<false>(a, p, s);
     if (e != hipSuccess || p.c.split == 1) return e;
