@@ -430,11 +430,6 @@ bool linear_size_ok(int T, int k, int n)
     return T >= 1 && T <= kLinearMaxT && k >= 8 && k % 8 == 0 && k <= kLinearMaxK && n >= 1 && n <= kLinearMaxN;
 }
 
-size_t linear_ws_bytes(int T, int k, int n)
-{
-    return T <= kStreamTokens ? 0 : up(linear_tile_ws_bytes(T, k, n));
-}
-
 bool few_size_ok(int T, int d, int f, int E, int k, int S)
 {
     return T >= 1 && T <= kFewTokens && d >= 8 && d % 8 == 0 && d <= 16384 && f >= 8 && f % 8 == 0 && E >= 1 &&
@@ -522,7 +517,7 @@ size_t moe_workspace_size(moe_op op, int T, int d, int f, int E, int k, int S)
     case MOE_OP_EAMC:
         return d > kEamcMaxLen ? 0 : up((size_t)T * 8);   // T stored EAMs of d entries
     case MOE_OP_LINEAR:
-        return linear_size_ok(T, d, f) ? linear_ws_bytes(T, d, f) : 0;
+        return linear_size_ok(T, d, f) ? up(linear_ws_bytes(T, d, f)) : 0;
     case MOE_OP_LAYER_FEW:
         return few_size_ok(T, d, f, E, k, S) ? few_ws_bytes(T, d, f, E, k, S, nullptr, nullptr) : 0;
     }
@@ -1011,7 +1006,7 @@ moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt,
     if (!aligned(x, 16) || x_stride % 8 != 0 || !aligned(L->w, 16) || !aligned(L->w_gate, 16) || !aligned(y, ya) ||
         !aligned(residual, ya) || !aligned(L->bias, 4) || !aligned(L->bias_gate, 4))
         return MOE_ERR_ALIGNMENT;
-    const size_t need = linear_ws_bytes(T, k, n);
+    const size_t need = up(linear_ws_bytes(T, k, n));
     if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return MOE_ERR_ALIGNMENT;
     LinearArgs a{};
@@ -1025,7 +1020,7 @@ moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt,
     a.y = y; a.ys = y_stride;
     a.part = (float *)ws;
     hipStream_t s = (hipStream_t)stream;
-    return hip_status(T <= kStreamTokens ? launch_linear_stream(a, s) : launch_linear_tile(a, s));
+    return hip_status(launch_linear(a, s));
 }
 
 moe_status moe_pack_up_int2(const void *w_up_t, moe_dtype dt, int d, int f, uint8_t *up_q,

@@ -528,15 +528,19 @@ hipError_t gateup(const FewArgs &a, hipStream_t s)
 {
     const int blocks = (a.d + 63) / 64, fb = (a.f + 15) / 16;
     const long long units = (long long)fb * a.amax;
+    constexpr int kMost = 160 * 1024;
+    static_assert(4 * kUpRing(XM) <= kMost, "four waves' rings fit a compute unit");
+    const size_t rb = ROUTE == kFromList ? 0 : route_bytes(a.T, a.E, a.k);
+    const size_t list = ROUTE == kFromRouter ? 16 * (size_t)(a.amax + 1) : 0;
+    // slices of d, as the linear layer's of K
     int P = 4;
-    while (P < 8 && units * P < 2048 && blocks >= 8 * P) P *= 2;
+    if (8 * kUpRing(XM) + list <= kMost && units * P < 2048 && blocks >= 8 * P) P = 8;
     while (P > 1 && blocks < P) P /= 2;
     const int G = P < 4 ? 4 / P : 1, slice = (blocks + P - 1) / P;
     static_assert(kUpRing(XM) >= (XM + 15) / 16 * 2048, "the sums fit the rings");
     size_t lds = (size_t)G * P * kUpRing(XM);
-    const size_t rb = ROUTE == kFromList ? 0 : route_bytes(a.T, a.E, a.k);
     if (rb > lds) lds = rb;
-    if (ROUTE == kFromRouter) lds += 16 * (size_t)(a.amax + 1);
+    lds += list;
     const hipError_t e = allow_lds((const void *)few_gateup_kernel<BF16, XM, ROUTE>, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((few_gateup_kernel<BF16, XM, ROUTE>), dim3((unsigned)((units + G - 1) / G)), dim3(64 * G * P),

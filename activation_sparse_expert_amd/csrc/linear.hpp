@@ -23,12 +23,9 @@ struct LinearArgs {
     float *part;                        // split of K: partial products (workspace)
 };
 
-// Rows up to which a call streams the weights past all tokens at once.
-constexpr int kStreamTokens = 32;
-
-hipError_t launch_linear_stream(const LinearArgs &a, hipStream_t s);    // T <= kStreamTokens
-hipError_t launch_linear_tile(const LinearArgs &a, hipStream_t s);      // any T
-size_t linear_tile_ws_bytes(int T, int K, int N);       // the larger of the plain and the gated call's
+hipError_t launch_linear(const LinearArgs &a, hipStream_t s);
+hipError_t launch_linear_stream(const LinearArgs &a, hipStream_t s);    // no workspace
+size_t linear_ws_bytes(int T, int K, int N);            // enough for the plain and the gated call
 
 // The few-token MoE layer: the experts of a call and their tokens, made from the
 // routing once.  Experts with tokens are listed in ascending order, the shared ones

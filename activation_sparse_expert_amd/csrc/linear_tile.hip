@@ -9,10 +9,10 @@
 // a token and stores them together.
 //
 // Two kernels.  Large products take 256 x 256 tiles and 8 waves in two groups
-// half a step apart (linear_big_kernel).  The others take smaller tiles with
-// several blocks in flight (linear_tile_kernel); where those are few, K is split
-// over workgroups, whose fp32 products a second kernel adds in a fixed order
-// before the epilogue.
+// a phase apart (linear_big_kernel).  The others take smaller tiles
+// (linear_tile_kernel); where those are few, K is split over workgroups, whose
+// fp32 products a second kernel adds in a fixed order before the epilogue.
+// plan() chooses by what each was measured to cost.
 #include "linear_epilogue.hpp"
 
 namespace moeffn {
@@ -65,16 +65,15 @@ __device__ __forceinline__ Place place(const Cut &c)
     return p;
 }
 
-// This lane's source (at k = 0) of 8 rows that a copy instruction fills: lane l
-// row l / 8, chunk l % 8 as stored.  Rows past the last token or output repeat it.
-template <int ON, int BM, bool GATED>
-__device__ __forceinline__ const uint16_t *row_source(const LinearArgs &a, int t0, int n0, int row, int lane)
+// copy16_to_lds with the source as a scalar base and a 32-bit byte offset per
+// lane, so that a block costs no vector arithmetic.
+__device__ __forceinline__ void copy16_to_lds_at(const void *base, uint32_t off, void *lds_base)
 {
-    const int k = 8 * ((lane & 7) ^ swizzle(row));
-    if (row < BM) return a.x + (size_t)min(t0 + row, a.T - 1) * a.xs + k;
-    const int br = row - BM;
-    const bool gate = GATED && br >= ON;
-    return (gate ? a.wg : a.w) + (size_t)min(n0 + (gate ? br - ON : br), a.N - 1) * a.K + k;
+    typedef __attribute__((address_space(3))) void lvoid;
+    const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lvoid *)lds_base);
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(m)
+                 : "m0", "memory");
 }
 
 // Epilogue of a wave's subtiles (value r of lane l of a subtile is output
@@ -131,15 +130,18 @@ __device__ __forceinline__ void store_tile(const LinearArgs &a, const Cut &c, in
     }
 }
 
-// S stages: blocks kb + 1 .. kb + S - 1 are in flight while block kb is multiplied.
+// S stages.  While block kb is multiplied the fragments of block kb + 1 are read
+// from LDS and blocks kb + 2 .. kb + S are in flight; a barrier a block.
 template <bool BF16, int BM, int BN, int WM, int WN, bool GATED, int S>
-__global__ void __launch_bounds__(64 * WM * WN)
+__global__ void __launch_bounds__(64 * WM * WN, 2)
 linear_tile_kernel(LinearArgs a, Cut c)
 {
     constexpr int W = WM * WN, ON = GATED ? BN / 2 : BN;
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32, HN = GATED ? TN / 2 : TN;
-    constexpr int kStage = (BM + BN) * 128, NI = (BM + BN) / 8 / W;
-    static_assert((BM + BN) % (8 * W) == 0 && (!GATED || TN % 2 == 0), "tile");
+    constexpr int kStage = (BM + BN) * 128, NI = (BM + BN) / 8 / W, KS = kKB / 16;
+    constexpr int NX = BM / 8 / W;                  // copies of token rows; then weight rows
+    static_assert(S >= 2, "stages");
+    static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0 && (!GATED || (TN % 2 == 0 && ON % (8 * W) == 0)), "tile");
     extern __shared__ __align__(16) unsigned char smem[];   // [S][kStage]
     const Place at = place(c);
     if (at.none) return;
@@ -148,27 +150,47 @@ linear_tile_kernel(LinearArgs a, Cut c)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;
-    const int kb0 = at.ks * c.blocks, kb1 = min(kb0 + c.blocks, (a.K + kKB - 1) / kKB);
+    const int nkb = (a.K + kKB - 1) / kKB, kb0 = at.ks * c.blocks, kb1 = min(kb0 + c.blocks, nkb);
 
-    const uint16_t *src[NI];
-    int ck[NI];
+    // copy q of this wave fills rows 8 (wave + W q) .. of the stage; sources as byte
+    // offsets from the tile's first token and weight rows
+    const uint16_t *xb = a.x + (size_t)t0 * a.xs;
+    const uint16_t *wb[2] = {a.w + (size_t)n0 * a.K, (GATED ? a.wg : a.w) + (size_t)n0 * a.K};
+    uint32_t off[NI];
 #pragma unroll
     for (int q = 0; q < NI; ++q) {
-        const int row = 8 * (wave + W * q) + (lane >> 3);
-        src[q] = row_source<ON, BM, GATED>(a, t0, n0, row, lane) + (size_t)kb0 * kKB;
-        ck[q] = 8 * ((lane & 7) ^ swizzle(row));
+        const int row = 8 * (wave + W * q) + (lane >> 3), k = 8 * ((lane & 7) ^ swizzle(row));
+        if (q < NX) off[q] = 2u * (uint32_t)(min(row, a.T - 1 - t0) * a.xs + k);
+        else off[q] = 2u * (uint32_t)(min((row - BM) % ON, a.N - 1 - n0) * a.K + k);
     }
-    int put = 0, next = kb0;
+    // In a last block that K does not fill, lanes past K copy the row's last 8
+    // values; once landed, zeros take their place.
+    const int left = a.K - (nkb - 1) * kKB;         // k values of the last block
+    auto past = [&](int q) { return 8 * ((lane & 7) ^ swizzle(8 * (wave + W * q) + (lane >> 3))) - (left - 8); };
+    int next = kb0, put = 0;                        // the block that is copied next, and its stage
     auto issue = [&]() {
-        unsigned char *base = smem + put * kStage;
-        put = put + 1 == S ? 0 : put + 1;
-        const bool tail = (next + 1) * kKB > a.K;
+        unsigned char *base = smem + put * kStage + 1024 * wave;
+        const bool tail = next == nkb - 1 && left < kKB;
 #pragma unroll
         for (int q = 0; q < NI; ++q) {
-            copy16_to_lds(tail && next * kKB + ck[q] >= a.K ? st::zeros16 : src[q], base + 1024 * (wave + W * q));
-            src[q] += kKB;
+            uint32_t o = off[q];
+            if (tail) o -= 2u * (uint32_t)max(past(q), 0);
+            const uint16_t *b = q < NX ? xb : wb[GATED && 8 * W * (q - NX) >= ON];
+            copy16_to_lds_at(b + (size_t)next * kKB, o, base + 1024 * W * q);
         }
+        put = put + 1 == S ? 0 : put + 1;
         ++next;
+    };
+    // this wave's copies of block kb have landed, `stage` being its stage
+    auto landed = [&](int kb, int stage) {
+        if (next - kb >= S - 1) st::wait_copies<NI * (S - 2)>();    // the S - 2 blocks after it may not have
+        else st::wait_copies<0>();
+        if (kb == nkb - 1 && left < kKB) {
+            unsigned char *base = smem + stage * kStage + 1024 * wave + 16 * lane;
+#pragma unroll
+            for (int q = 0; q < NI; ++q)
+                if (past(q) > 0) *(uint4 *)(base + 1024 * W * q) = make_uint4(0, 0, 0, 0);
+        }
     };
 
     floatx16 acc[TM][TN];
@@ -186,47 +208,57 @@ linear_tile_kernel(LinearArgs a, Cut c)
 #pragma unroll
     for (int j = 0; j < TN; ++j)
         brow[j] = BM + (j < HN ? 32 * HN * wn + 32 * j : ON + 32 * HN * wn + 32 * (j - HN)) + li;
-
+    struct Frags {
+        uint4 a[TM][KS], b[TN][KS];
+    };
+    auto read = [&](Frags &f, int stage) {
+        const unsigned char *stg = smem + stage * kStage;
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s)
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) f.a[i][s] = *(const uint4 *)(stg + lds_at(arow[i], 2 * s + hk));
+#pragma unroll
+            for (int j = 0; j < TN; ++j) f.b[j][s] = *(const uint4 *)(stg + lds_at(brow[j], 2 * s + hk));
+        }
+    };
+    int get = 0;                                    // stage of the block that is read next
+    // the block in f, while the next one goes into g
+    auto step = [&](int kb, Frags &f, Frags &g) {
+        const bool more = kb + 1 < kb1;
+        if (more) landed(kb + 1, get);
+        // every wave has read block kb, whose stage is filled next, and can read block kb + 1
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (more) {
+            read(g, get);
+            get = get + 1 == S ? 0 : get + 1;
+        }
         if (next < kb1) issue();
-    int get = 0;
-    for (int kb = kb0; kb < kb1; ++kb) {
-        // block kb has landed, and every wave is done with block kb - 1, whose stage is filled next
-        if (next - kb >= S - 1) st::wait_copies<NI * (S - 2)>();
-        else st::wait_copies<0>();
-        __syncthreads();
-        if (next < kb1) issue();
-        const unsigned char *stg = smem + get * kStage;
-        get = get + 1 == S ? 0 : get + 1;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int s = 0; s < kKB / 16; ++s) {
-            uint4 av[TM], bv[TN];
-#pragma unroll
-            for (int i = 0; i < TM; ++i) av[i] = *(const uint4 *)(stg + lds_at(arow[i], 2 * s + hk));
-#pragma unroll
-            for (int j = 0; j < TN; ++j) bv[j] = *(const uint4 *)(stg + lds_at(brow[j], 2 * s + hk));
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mma32<BF16>(bv[j], av[i], acc[i][j]);
-        }
+                for (int j = 0; j < TN; ++j) acc[i][j] = mma32<BF16>(f.b[j][s], f.a[i][s], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+        if (next < kb1) issue();
+    Frags f0, f1;
+    landed(kb0, 0);
+    __syncthreads();
+    read(f0, 0);
+    get = 1;
+    for (int kb = kb0; kb < kb1; kb += 2) {
+        step(kb, f0, f1);
+        if (kb + 1 < kb1) step(kb + 1, f1, f0);
     }
     __syncthreads();                                // the stages are done with
     static_assert(W * kWaveLds(TN) <= S * kStage, "the epilogue fits the stages");
     store_tile<TM, TN, GATED>(a, c, at.ks, t0 + BM / WM * wm, n0 + 32 * HN * wn, lane,
                               (float *)(smem + wave * kWaveLds(TN)), acc);
-}
-
-// copy16_to_lds with the source as a scalar base and a 32-bit byte offset per
-// lane, so that a block costs no vector arithmetic.
-__device__ __forceinline__ void copy16_to_lds_at(const void *base, uint32_t off, void *lds_base)
-{
-    typedef __attribute__((address_space(3))) void lvoid;
-    const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lvoid *)lds_base);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                 :: "v"(off), "s"(base), "s"(m)
-                 : "m0", "memory");
 }
 
 // 256 x 256 tiles, 8 waves of 128 tokens x 64 weight rows each (4 x 2 subtiles).
@@ -377,32 +409,57 @@ linear_join_kernel(LinearArgs a, int split)
     le::finish(a, t, n, v[0], v[1]);
 }
 
-// Tile sizes by the number of tiles they give: 256 x 256 weight rows, 128 x
-// 128, or 64 x 64 outputs while those leave compute units idle.
+// The tiles that a call can take, and what a block of 64 k costs a compute unit, in
+// microseconds as measured: one workgroup alone on it, and two together where
+// two fit.  (Alone, a small tile waits: for its barrier, LDS and a chain of MFMAs.)
+struct Tile {
+    int bm, bn;                                     // tokens x weight rows
+    double one, two;                                // two: 0 where one workgroup's LDS fills the unit
+};
+constexpr Tile kTiles[] = {{64, 64, 0.40, 0.55}, {128, 64, 0.50, 0.75}, {128, 128, 1.05, 1.25}, {128, 256, 1.0, 0.0},
+                           {256, 256, 1.75, 0.0}};
+constexpr int kUnits = 256;                         // compute units
+
 struct Plan {
-    int bm;                                         // 256, 128 or 64
+    int tile;                                       // of kTiles
     Cut c;
 };
 
 constexpr int kMaxSplit = 8;
+constexpr long long kTileStride = 1 << 21;          // elements: 256 rows within 1 GB
 
-// big_ok: the offsets of a 256-row tile fit 32 bits (linear_big_kernel)
-Plan plan(int T, int K, int N, bool gated, bool big_ok)
+// The tile and split of K with the least expected time: rounds of workgroups over the
+// compute units, and for a split the second kernel (4 us) and the products written
+// and read at 4 TB/s.
+Plan plan(int T, int K, int N, bool gated)
 {
-    const int nkb = (K + kKB - 1) / kKB;
-    auto tiles = [&](int m, int n) { return (long long)((T + m - 1) / m) * ((N + n - 1) / n); };
-    const int g = gated ? 2 : 1;
-    Plan p{};
-    p.bm = big_ok && tiles(256, 256 / g) >= 192 ? 256 : tiles(128, 128 / g) >= 256 ? 128 : 64;
-    const int on = p.bm == 64 ? 64 : p.bm / g;
-    p.c.tm = (T + p.bm - 1) / p.bm;
-    p.c.tn = (N + on - 1) / on;
-    int split = 1;
-    if (p.bm == 64)
-        while (split < kMaxSplit && (long long)p.c.tm * p.c.tn * split < 256 && nkb >= 16 * split) split *= 2;
-    p.c.blocks = (nkb + split - 1) / split;
-    p.c.split = (nkb + p.c.blocks - 1) / p.c.blocks;
-    return p;
+    const int nkb = (K + kKB - 1) / kKB, g = gated ? 2 : 1;
+    Plan best{};
+    double least = 1e30;
+    for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+        const Tile &t = kTiles[i];
+        Cut c{};
+        c.tm = (T + t.bm - 1) / t.bm;
+        c.tn = (N + t.bn / g - 1) / (t.bn / g);
+        for (int want = 1; want <= (t.bm == 256 ? 1 : kMaxSplit); want *= 2) {
+            if (want > 1 && nkb < 4 * want) break;
+            c.blocks = (nkb + want - 1) / want;
+            c.split = (nkb + c.blocks - 1) / c.blocks;
+            const long long wgs = (long long)c.tm * c.tn * c.split;
+            const int per = t.two > 0.0 ? 2 * kUnits : kUnits;
+            const long long rest = wgs % per;
+            double us = (double)(wgs / per) * (t.two > 0.0 ? t.two : t.one);
+            if (rest > kUnits) us += t.two;
+            else if (rest > 0) us += t.one;
+            us *= c.blocks;
+            if (c.split > 1) us += 4.0 + 8e-6 * c.split * g * (double)T * N / 4.0;
+            if (us < least) {
+                least = us;
+                best = Plan{i, c};
+            }
+        }
+    }
+    return best;
 }
 
 hipError_t launch_cut(const void *k, const LinearArgs &a, const Cut &c, int threads, int lds, hipStream_t s)
@@ -417,36 +474,60 @@ hipError_t launch_cut(const void *k, const LinearArgs &a, const Cut &c, int thre
     return e != hipSuccess ? e : hipGetLastError();
 }
 
-template <bool BF16, int BM, int BN, bool GATED, int S>
+template <bool BF16, int BM, int BN, int WM, int WN, bool GATED, int S>
 hipError_t launch_tile(const LinearArgs &a, const Cut &c, hipStream_t s)
 {
-    return launch_cut((const void *)linear_tile_kernel<BF16, BM, BN, 2, 2, GATED, S>, a, c, 256, S * (BM + BN) * 128, s);
+    return launch_cut((const void *)linear_tile_kernel<BF16, BM, BN, WM, WN, GATED, S>, a, c, 64 * WM * WN,
+                      S * (BM + BN) * 128, s);
 }
 
 template <bool BF16>
 hipError_t launch_t(const LinearArgs &a, const Plan &p, hipStream_t s)
 {
-    if (p.bm == 256)
-        return launch_cut(a.wg ? (const void *)linear_big_kernel<BF16, true> : (const void *)linear_big_kernel<BF16, false>,
-                          a, p.c, 512, 2 * 512 * 128, s);
-    if (p.bm == 128)
-        return a.wg ? launch_tile<BF16, 128, 128, true, 2>(a, p.c, s) : launch_tile<BF16, 128, 128, false, 2>(a, p.c, s);
-    return a.wg ? launch_tile<BF16, 64, 128, true, 3>(a, p.c, s) : launch_tile<BF16, 64, 64, false, 4>(a, p.c, s);
+    switch (p.tile) {
+    case 0:
+        return a.wg ? launch_tile<BF16, 64, 64, 2, 1, true, 4>(a, p.c, s)
+                    : launch_tile<BF16, 64, 64, 2, 2, false, 4>(a, p.c, s);
+    case 1:
+        return a.wg ? launch_tile<BF16, 128, 64, 4, 1, true, 3>(a, p.c, s)
+                    : launch_tile<BF16, 128, 64, 2, 2, false, 3>(a, p.c, s);
+    case 2:
+        return a.wg ? launch_tile<BF16, 128, 128, 2, 2, true, 2>(a, p.c, s)
+                    : launch_tile<BF16, 128, 128, 2, 2, false, 2>(a, p.c, s);
+    case 3:
+        return a.wg ? launch_tile<BF16, 128, 256, 2, 4, true, 3>(a, p.c, s)
+                    : launch_tile<BF16, 128, 256, 2, 4, false, 3>(a, p.c, s);
+    }
+    return launch_cut(a.wg ? (const void *)linear_big_kernel<BF16, true> : (const void *)linear_big_kernel<BF16, false>, a,
+                      p.c, 512, 2 * 512 * 128, s);
+}
+
+// Whether a call streams its weights past the tokens (linear_stream.hip) instead:
+// up to 32 tokens, whose tiles would be half empty, and small products whose
+// token tiles of 32 and groups of 16 outputs give each compute unit one workgroup
+// at most (4096 x 1024 at 128 tokens: 8.8 us against 12.0 in tiles; with 267
+// workgroups at 2056 x 1411 and 77 tokens 11.6 against 10.6).
+bool streams(int T, int K, int N)
+{
+    return T <= 32 || (K <= 8192 && (long long)((T + 31) / 32) * ((N + 15) / 16) <= kUnits);
 }
 
 }  // namespace
 
-size_t linear_tile_ws_bytes(int T, int K, int N)
+size_t linear_ws_bytes(int T, int K, int N)
 {
-    const Plan p = plan(T, K, N, false, true), g = plan(T, K, N, true, true);
+    if (streams(T, K, N)) return 0;
+    const Plan p = plan(T, K, N, false), g = plan(T, K, N, true);
     const size_t np = p.c.split > 1 ? p.c.split : 0, ng = g.c.split > 1 ? 2 * g.c.split : 0;
     return (np > ng ? np : ng) * (size_t)T * N * 4;
 }
 
-hipError_t launch_linear_tile(const LinearArgs &a, hipStream_t s)
+hipError_t launch_linear(const LinearArgs &a, hipStream_t s)
 {
     if (a.T < 1 || a.K < 8 || a.K % 8 != 0 || a.N < 1) return hipErrorInvalidValue;
-    Plan p = plan(a.T, a.K, a.N, a.wg != nullptr, a.xs <= (1 << 21));
+    // (the offsets of a tile's rows have 32 bits)
+    if (streams(a.T, a.K, a.N) || a.xs > kTileStride) return launch_linear_stream(a, s);
+    Plan p = plan(a.T, a.K, a.N, a.wg != nullptr);
     p.c.quads = p.c.split > 1 ? a.N % 4 == 0 : le::quads(a);
     const hipError_t e = a.bf16 ? launch_t<true>(a, p, s) : launch_t<false>(a, p, s);
     if (e != hipSuccess || p.c.split == 1) return e;

@@ -26,8 +26,8 @@ def _linear(n=704, k=256, wdt=0, w=FAKE, bias=None, w_gate=None, bias_gate=None,
     (dict(x=FAKE + 8), -3), (dict(xs=260), -3), (dict(w=FAKE + 2), -3), (dict(w_gate=FAKE + 8), -3),
     (dict(y=FAKE + 2), -3), (dict(r=FAKE + 2), -3), (dict(bias=FAKE + 2), -3),
     (dict(w_gate=FAKE, bias_gate=FAKE + 1), -3),
-    (dict(T=40, k=8192, n=64, ws=None), -4), (dict(T=40, k=8192, n=64, ws_bytes=0), -4),
-    (dict(T=40, k=8192, n=64, ws_bytes=256), -4), (dict(ws=FAKE + 4), -3),
+    (dict(T=40, k=16384, n=64, ws=None), -4), (dict(T=40, k=16384, n=64, ws_bytes=0), -4),
+    (dict(T=40, k=16384, n=64, ws_bytes=256), -4), (dict(ws=FAKE + 4), -3),
 ])
 def test_linear_rejects(kw, code):
     assert _linear(**kw) == code

@@ -77,7 +77,8 @@ SHAPES = [  # T, d, f, E, k, S
     (1, 8, 8, 1, 1, 0), (1, 256, 704, 4, 2, 1), (1, 2048, 1408, 64, 6, 2), (2, 264, 72, 5, 5, 0),
     (4, 1000, 712, 17, 3, 1), (13, 520, 328, 40, 4, 2), (16, 4096, 256, 8, 2, 0), (17, 136, 1000, 9, 2, 1),
     (31, 2048, 264, 64, 6, 2), (32, 512, 96, 130, 8, 0), (32, 64, 40, 1024, 1, 1), (32, 128, 64, 3, 1, 3),
-    (1, 72, 200, 1000, 3, 0), (1, 64, 40, 40, 20, 1), (3, 64, 40, 70, 17, 0), (20, 96, 136, 2, 2, 1)]
+    (1, 72, 200, 1000, 3, 0), (1, 64, 40, 40, 20, 1), (3, 64, 40, 70, 17, 0), (20, 96, 136, 2, 2, 1),
+    (20, 2048, 264, 4, 2, 1), (10, 2056, 264, 4, 2, 1), (5, 4096, 72, 3, 1, 2)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])

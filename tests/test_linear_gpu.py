@@ -43,7 +43,8 @@ def want(lin, x, residual, out):
 SIZES = [(1, 8, 1), (1, 256, 704), (2, 40, 17), (16, 2056, 15), (17, 264, 33), (32, 1000, 129), (5, 4096, 1411),
          (33, 8, 1), (33, 72, 65), (64, 256, 64), (65, 1032, 127), (100, 2056, 1411), (128, 512, 128),
          (129, 64, 257), (257, 136, 300), (300, 4096, 512), (1000, 520, 1000), (2050, 72, 2049),
-         (3000, 8, 4207), (3000, 200, 4208), (2900, 1000, 4207)]
+         (3000, 8, 4207), (3000, 200, 4208), (2900, 1000, 4207),
+         (20, 4096, 1411), (24, 2056, 4000), (30, 2056, 16500), (24, 2056, 16400), (96, 1024, 512), (2, 16384, 40)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
