@@ -2,8 +2,8 @@
 // and FloE review, "MoE 专家前向计算": top-k routing, SwiGLU experts):
 //   y_t = r_t + sum_s w_ts a_e(t,s)(x_t) + sum_i a_E+i(x_t),
 //   a_e(x) = (SiLU(x G_e) (.) (x U_e)) D_e.
-// Bound by the weights of the chosen experts, read once past the tokens that
-// chose each (mfma_stream.hpp), in two kernels:
+// Bound by the weights of the chosen experts, streamed past the tokens that chose
+// each (mfma_stream.hpp), in two kernels:
 //   gate/up: a wave takes 16 channels of a listed expert and a slice of d;
 //            h = SiLU(g) u goes to the workspace;
 //   down:    a workgroup takes 16 columns of y and a share of the listed

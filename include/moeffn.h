@@ -338,7 +338,8 @@ moe_status moe_layer_forward(const moe_layer *L, const void *x, moe_dtype xdt, i
  *   y_t = residual_t + sum_s w_{t,s} a_{e(t,s)}(x_t) + sum_i a_{E+i}(x_t),
  *   a_e(x) = (SiLU(x W^gate) (.) x W^up) W^down
  * (FloE review, "MoE 专家前向计算"; routing as moe_route_topk).  The weights of
- * the experts that some token chose are read once, whatever the tokens.
+ * the experts that some token chose are read once, whatever the tokens, but
+ * that an expert with more than 16 tokens reads W^down twice.
  * Of L it reads d, f (both multiples of 8), n_routed, n_shared, top_k,
  * renormalize, wdt, the router, gate_t, up_dense and down_dense, which all have
  * to be there; the INT2 codes, `down` and the thresholds are not read and may be
@@ -369,7 +370,8 @@ moe_status moe_layer_forward_few(const moe_layer *L, const void *x, moe_dtype xd
  *   the same stride; y must not overlap x or the weights otherwise.
  * Limits: 1 <= T <= 65536; k a multiple of 8 up to 2^20, n up to 2^24 (else
  * MOE_ERR_UNSUPPORTED); x and the weights 16-byte aligned.  The order of the
- * sums depends on T, n and k alone: outputs are bit-reproducible.
+ * sums depends on T, n, k, whether the layer is gated and (past 2^21) x_stride,
+ * never on values or addresses: outputs are bit-reproducible.
  * Workspace: moe_workspace_size(MOE_OP_LINEAR, T, k, n, 0, 0, 0) bytes, gated or
  * not; where that is 0 (up to 32 tokens, and wherever K is not split) ws may be NULL.
  */

@@ -78,7 +78,10 @@ SHAPES = [  # T, d, f, E, k, S
     (4, 1000, 712, 17, 3, 1), (13, 520, 328, 40, 4, 2), (16, 4096, 256, 8, 2, 0), (17, 136, 1000, 9, 2, 1),
     (31, 2048, 264, 64, 6, 2), (32, 512, 96, 130, 8, 0), (32, 64, 40, 1024, 1, 1), (32, 128, 64, 3, 1, 3),
     (1, 72, 200, 1000, 3, 0), (1, 64, 40, 40, 20, 1), (3, 64, 40, 70, 17, 0), (20, 96, 136, 2, 2, 1),
-    (20, 2048, 264, 4, 2, 1), (10, 2056, 264, 4, 2, 1), (5, 4096, 72, 3, 1, 2)]
+    (20, 2048, 264, 4, 2, 1), (10, 2056, 264, 4, 2, 1), (5, 4096, 72, 3, 1, 2),
+    # the limits: T (k + S), experts, inputs, choices worked out by every workgroup
+    (32, 64, 40, 1024, 63, 1), (32, 128, 64, 600, 32, 32), (32, 16384, 72, 6, 2, 0), (1, 64, 24, 1024, 16, 0),
+    (1, 64, 40, 5, 2, 700), (8, 8, 16, 512, 64, 0)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])

@@ -169,3 +169,23 @@ def test_far_offsets():
     y = big.view(T, stride)[:, 1024:1024 + n]
     moe.linear_forward(lin, x, y=y)
     check(y, *want(lin, x, None, torch.float16), "far")
+
+
+@pytest.mark.parametrize("stride", [2 ** 21, 2 ** 21 + 8])
+def test_rows_far_apart(stride):
+    """Both sides of the stride up to which the offsets of a tile's rows have 32 bits."""
+    g = gen(43)
+    T, k, n = 40, 72, 4112
+    lin = layer(g, n, k, torch.bfloat16, gated=True, act="silu")
+    x = torch.empty(T * stride, dtype=torch.bfloat16, device=DEV).view(T, stride)[:, :k]
+    x.copy_(normal(g, (T, k), 1.0, torch.bfloat16))
+    check(moe.linear_forward(lin, x), *want(lin, x, None, torch.float32), "far rows")
+
+
+@pytest.mark.parametrize("T,k,n", [(60000, 8192, 1), (65536, 72, 24)])
+def test_many_tokens(T, k, n):
+    """The most tokens, and many whose products are split over K and joined."""
+    g = gen(47)
+    lin = layer(g, n, k, torch.bfloat16, bias=True)
+    x = normal(g, (T, k), 1.0, torch.bfloat16)
+    check(moe.linear_forward(lin, x), *want(lin, x, None, torch.float32), f"T={T}")
