@@ -218,6 +218,34 @@ def test_graph_replays_follow_their_inputs(T):
         assert torch.equal(y, eager), f"replay {i}"
 
 
+def test_two_graphs_share_a_workspace():
+    """Graphs of both operators that follow each other on one stream may use one workspace."""
+    g = gen(23)
+    bf = torch.bfloat16
+    d = 1024
+    L = make(g, d, 328, 12, 3, 1, bf)
+    lin = moe.Linear(normal(g, (d, 4 * d), d ** -0.5 / 2, bf))
+    x, z = normal(g, (9, d), 1.0, bf), normal(g, (200, 4 * d), 1.0, bf)
+    split = moe.workspace_size(moe.OP_LINEAR, 200, 4 * d, d)
+    assert split > 0
+    ws = moe.new_workspace(max(moe.workspace_size(moe.OP_LAYER_FEW, 9, d, 328, 12, 3, 1), split))
+    y, v = torch.empty((9, d), dtype=bf, device=DEV), torch.empty((200, d), dtype=bf, device=DEV)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graphs[0]):
+        moe.layer_forward_few(L, x, y=y, ws=ws)
+    with torch.cuda.graph(graphs[1]):
+        moe.linear_forward(lin, z, y=v, ws=ws)
+    for i in range(3):
+        x.copy_(normal(g, (9, d), 1.0, bf))
+        z.copy_(normal(g, (200, 4 * d), 1.0, bf))
+        a, b = moe.layer_forward_few(L, x, out_dtype=bf), moe.linear_forward(lin, z, out_dtype=bf)
+        for graph in graphs + graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, a) and torch.equal(v, b), f"replay {i}"
+
+
 def test_two_streams_with_their_own_workspaces():
     g = gen(13)
     L = make(g, 1024, 512, 16, 2, 1, torch.bfloat16)

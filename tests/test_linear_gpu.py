@@ -182,10 +182,11 @@ def test_rows_far_apart(stride):
     check(moe.linear_forward(lin, x), *want(lin, x, None, torch.float32), "far rows")
 
 
-@pytest.mark.parametrize("T,k,n", [(60000, 8192, 1), (65536, 72, 24)])
+@pytest.mark.parametrize("T,k,n", [(33000, 2048, 1), (33000, 4096, 40), (65536, 72, 24)])
 def test_many_tokens(T, k, n):
     """The most tokens, and many whose products are split over K and joined."""
     g = gen(47)
-    lin = layer(g, n, k, torch.bfloat16, bias=True)
+    assert (moe.workspace_size(moe.OP_LINEAR, T, k, n) > 0) == (k > 72)
+    lin = layer(g, n, k, torch.bfloat16, gated=True, bias=True, act="silu")
     x = normal(g, (T, k), 1.0, torch.bfloat16)
     check(moe.linear_forward(lin, x), *want(lin, x, None, torch.float32), f"T={T}")
