@@ -13,8 +13,8 @@
 // (linear_tile_kernel); where those are few, K is split over workgroups, whose
 // fp32 products a second kernel adds in a fixed order before the epilogue.
 // plan() chooses by what each was measured to cost.
-// 4096 x 4096 x (2 x 14336), gated: 781-814 us, 1180-1230 TFLOP/s (MFMA busy 62%
-// of the cycles at the 1.8 GHz that the power limit leaves).  300 x 4096 x 4096:
+// 4096 x 4096 x (2 x 14336), gated: 780-850 us, 1130-1230 TFLOP/s (MFMA busy 62%
+// of the cycles at the 1.75 GHz that the power limit leaves).  300 x 4096 x 4096:
 // 24 us in 128 x 256 tiles and 4 parts of K, and 5.6 us for their sum: a block of 64
 // k waits for its barrier, its fragments and its MFMAs in turn (1.0 us, of which
 // the MFMAs are 0.43).
@@ -404,7 +404,7 @@ constexpr int kMaxSplit = 8;
 // Sum of the split's products, in order, and the epilogue: a thread takes four outputs
 // of a token where they can be read and written together (Q 4), else one, and
 // loads all their products before it uses the first (4096 outputs of 300 tokens
-// in two parts: 5.6 us, against 8.4 by single outputs and loads).
+// in four parts: 5.6 us, against 8.4 by single outputs and loads).
 template <int Q>
 __global__ void __launch_bounds__(256)
 linear_join_kernel(LinearArgs a, int split)
