@@ -26,6 +26,7 @@ namespace {
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
+constexpr int kLgkm0 = 0xC07F;                      // s_waitcnt lgkmcnt(0)
 constexpr int kKB = 64;                             // k values per block: 128-byte rows
 
 template <bool BF16>
@@ -216,15 +217,12 @@ linear_tile_kernel(LinearArgs a, Cut c)
     struct Frags {
         uint4 a[TM][KS], b[TN][KS];
     };
-    auto read = [&](Frags &f, int stage) {
+    auto read = [&](Frags &f, int stage, int s) {   // 16 of a block's 64 k
         const unsigned char *stg = smem + stage * kStage;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
+        for (int i = 0; i < TM; ++i) f.a[i][s] = *(const uint4 *)(stg + lds_at(arow[i], 2 * s + hk));
 #pragma unroll
-            for (int i = 0; i < TM; ++i) f.a[i][s] = *(const uint4 *)(stg + lds_at(arow[i], 2 * s + hk));
-#pragma unroll
-            for (int j = 0; j < TN; ++j) f.b[j][s] = *(const uint4 *)(stg + lds_at(brow[j], 2 * s + hk));
-        }
+        for (int j = 0; j < TN; ++j) f.b[j][s] = *(const uint4 *)(stg + lds_at(brow[j], 2 * s + hk));
     };
     int get = 0;                                    // stage of the block that is read next
     // the block in f, while the next one goes into g
@@ -232,20 +230,23 @@ linear_tile_kernel(LinearArgs a, Cut c)
         const bool more = kb + 1 < kb1;
         if (more) landed(kb + 1, get);
         // every wave has read block kb, whose stage is filled next, and can read block kb + 1
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (more) {
-            read(g, get);
-            get = get + 1 == S ? 0 : get + 1;
-        }
-        if (next < kb1) issue();
-        __builtin_amdgcn_sched_barrier(0);
+        // (a builtin, so that the compiler knows that f has arrived and does not wait
+        // for g as well before it multiplies f)
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(kLgkm0);
+        asm volatile("s_barrier" ::: "memory");
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+        for (int s = 0; s < KS; ++s) {
+            if (more) read(g, get, s);
+            if (s == 0 && next < kb1) issue();
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int j = 0; j < TN; ++j) acc[i][j] = mma32<BF16>(f.b[j][s], f.a[i][s], acc[i][j]);
-        __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        get = get + 1 == S ? 0 : get + 1;
     };
 
 #pragma unroll
@@ -254,7 +255,8 @@ linear_tile_kernel(LinearArgs a, Cut c)
     Frags f0, f1;
     landed(kb0, 0);
     __syncthreads();
-    read(f0, 0);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) read(f0, 0, s);
     get = 1;
     for (int kb = kb0; kb < kb1; kb += 2) {
         step(kb, f0, f1);
@@ -266,71 +268,77 @@ linear_tile_kernel(LinearArgs a, Cut c)
                               (float *)(smem + wave * kWaveLds(TN)), acc);
 }
 
-// 256 x 256 tiles, 8 waves of 128 tokens x 64 weight rows each (4 x 2 subtiles).
-// A block of 64 k takes a wave two phases, a barrier of the workgroup after each:
-// it reads its 24 fragments, then multiplies them (32 MFMAs, 1024 cycles).
-// Waves 4-7 run one phase behind waves 0-3 and every SIMD holds one of each, so
-// that while one group multiplies the other reads LDS: 192 KB a block, with 64 KB
-// written, which is all that LDS moves in the time of the MFMAs and would bound the
-// tile by itself if the two did not overlap.  (Four phases of 16 MFMAs, whose
-// barriers and first reads each cost about 270 cycles, took 3100 cycles a block.)
-// The copies of block kb + 1 are issued when both groups have read block kb - 1,
-// two phases before they are needed.
-template <bool BF16, bool GATED>
+// Tiles of BM (256 or 128) tokens x 256 weight rows, 8 waves of BM / 2 tokens x 64 weight
+// rows each (TM x 2 subtiles).  A block of 64 k takes a wave two phases, a barrier
+// of the workgroup after each: it reads its fragments, then multiplies them
+// (32 or 16 MFMAs).  Waves 4-7 run one phase behind waves 0-3 and every SIMD holds
+// one of each, so that while one group multiplies the other reads LDS: in the 256
+// x 256 tile 192 KB a block, with 64 KB written, which is all that LDS moves in
+// the time of the MFMAs and would bound the tile by itself if the two did not
+// overlap.  (There four phases of 16 MFMAs, whose barriers and first reads each cost
+// about 270 cycles, took 3100 cycles a block.)
+// S stages: the copies of block kb + S - 1 are issued when both groups have read
+// block kb - 1, two phases (S 2) or four before they are needed.
+template <bool BF16, bool GATED, int BM, int S>
 __global__ void __launch_bounds__(512, 2)
 linear_big_kernel(LinearArgs a, Cut c)
 {
-    constexpr int ON = GATED ? 128 : 256, HN = GATED ? 1 : 2;
-    constexpr int kStage = 512 * 128;
-    extern __shared__ __align__(16) unsigned char smem[];   // [2][256 token rows, 256 weight rows][128 B]
+    constexpr int ON = GATED ? 128 : 256, HN = GATED ? 1 : 2, TM = BM / 64;
+    constexpr int kStage = (BM + 256) * 128, NX = BM / 64, NI = NX + 4;
+    extern __shared__ __align__(16) unsigned char smem[];   // [S][BM token rows, 256 weight rows][128 B]
     const Place at = place(c);
     if (at.none) return;
-    const int t0 = at.t * 256, n0 = at.n * ON;
+    const int t0 = at.t * BM, n0 = at.n * ON;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    const int nkb = (a.K + kKB - 1) / kKB;
+    const int nkb = (a.K + kKB - 1) / kKB, kb0 = at.ks * c.blocks, kb1 = min(kb0 + c.blocks, nkb);
 
-    // copies 0-3 of this wave fill token rows 8 (wave + 8 q) .., 4-7 weight rows;
-    // sources as byte offsets from the tile's first row (launch_linear_tile sees to it
-    // that they fit)
+    // copies 0 .. NX - 1 of this wave fill token rows 8 (wave + 8 q) .., the others
+    // weight rows; sources as byte offsets from the tile's first row (launch_linear
+    // sees to it that they fit)
     const uint16_t *xb = a.x + (size_t)t0 * a.xs;
     const uint16_t *wb[2] = {a.w + (size_t)n0 * a.K, (GATED ? a.wg : a.w) + (size_t)n0 * a.K};
-    uint32_t off[8];
+    auto row_of = [&](int q) { return 8 * (wave + 8 * (q < NX ? q : q - NX)) + (lane >> 3); };
+    uint32_t off[NI];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const int row = 8 * (wave + 8 * (q & 3)) + (lane >> 3);
-        const int k = 8 * ((lane & 7) ^ swizzle(row));
-        if (q < 4) off[q] = 2u * (uint32_t)(min(row, a.T - 1 - t0) * a.xs + k);
+    for (int q = 0; q < NI; ++q) {
+        const int row = row_of(q), k = 8 * ((lane & 7) ^ swizzle(row));
+        if (q < NX) off[q] = 2u * (uint32_t)(min(row, a.T - 1 - t0) * a.xs + k);
         else off[q] = 2u * (uint32_t)(min(GATED ? row & 127 : row, a.N - 1 - n0) * a.K + k);
     }
     // In a last block that K does not fill, lanes past K copy the row's last 8
     // values; once landed, zero_tail puts zeros in their place.
     const int left = a.K - (nkb - 1) * kKB;         // k values of the last block
-    auto past = [&](int q) { return 8 * ((lane & 7) ^ swizzle(8 * (wave + 8 * (q & 3)) + (lane >> 3))) - (left - 8); };
+    auto past = [&](int q) { return 8 * ((lane & 7) ^ swizzle(row_of(q))) - (left - 8); };
+    int put = 0, get = 0;                           // stages of the block copied next and of the one read next
     auto copy_block = [&](int kb) {
-        unsigned char *st = smem + (kb & 1) * kStage + 1024 * wave;
+        unsigned char *st = smem + put * kStage + 1024 * wave;
+        put = put + 1 == S ? 0 : put + 1;
         const bool tail = kb == nkb - 1 && left < kKB;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const uint16_t *b = q < 4 ? xb : wb[GATED && q >= 6 ? 1 : 0];
+        for (int q = 0; q < NI; ++q) {
+            const uint16_t *b = q < NX ? xb : wb[GATED && q >= NX + 2 ? 1 : 0];
             uint32_t o = off[q];
             if (tail) o -= 2u * (uint32_t)max(past(q), 0);
             copy16_to_lds_at(b + (size_t)kb * kKB, o, st + 8192 * q);
         }
     };
-    auto zero_tail = [&](int kb) {
+    // this wave's copies of block kb, in stage `get`, have landed
+    auto landed = [&](int kb) {
+        if (kb + S - 2 < kb1) st::wait_copies<NI * (S - 2)>();      // all S - 2 blocks after it are in flight
+        else st::wait_copies<0>();
         if (kb != nkb - 1 || left == kKB) return;
-        unsigned char *st = smem + (kb & 1) * kStage + 1024 * wave + 16 * lane;
+        unsigned char *st = smem + get * kStage + 1024 * wave + 16 * lane;
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
+        for (int q = 0; q < NI; ++q)
             if (past(q) > 0) *(uint4 *)(st + 8192 * q) = make_uint4(0, 0, 0, 0);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     };
 
-    floatx16 acc[4][2];
+    floatx16 acc[TM][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -338,17 +346,19 @@ linear_big_kernel(LinearArgs a, Cut c)
     const int li = lane & 31, hk = lane >> 5;
     int brow[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) brow[j] = 256 + (GATED ? 128 * j + 32 * wn : 64 * wn + 32 * j) + li;
+    for (int j = 0; j < 2; ++j) brow[j] = BM + (GATED ? 128 * j + 32 * wn : 64 * wn + 32 * j) + li;
 
-    uint4 av[4][4], bv[2][4];
-    auto read_block = [&](int kb) {
-        const unsigned char *st = smem + (kb & 1) * kStage;
+    uint4 av[TM][4], bv[2][4];
+    auto read_block = [&]() {
+        const unsigned char *st = smem + get * kStage;
+        get = get + 1 == S ? 0 : get + 1;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) bv[j][s] = *(const uint4 *)(st + lds_at(brow[j], 2 * s + hk));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) av[i][s] = *(const uint4 *)(st + lds_at(128 * wm + 32 * i + li, 2 * s + hk));
+            for (int i = 0; i < TM; ++i)
+                av[i][s] = *(const uint4 *)(st + lds_at(32 * TM * wm + 32 * i + li, 2 * s + hk));
         }
     };
     auto multiply = [&]() {
@@ -357,46 +367,48 @@ linear_big_kernel(LinearArgs a, Cut c)
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) acc[i][j] = mma32<BF16>(bv[j][s], av[i][s], acc[i][j]);
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    copy_block(0);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    zero_tail(0);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i)
+        if (kb0 + i < kb1) copy_block(kb0 + i);
+    landed(kb0);
     asm volatile("s_barrier" ::: "memory");
-    // phase p of the workgroup: waves 0-3 read block p / 2 or multiply it, waves
+    // phase p of the workgroup: waves 0-3 read block kb0 + p / 2 or multiply it, waves
     // 4-7 do what those did in phase p - 1; both copy in even phases and have
-    // their copies waited for by the end of the odd ones
+    // waited by the end of the odd ones for what is read next
     if (wm == 0) {
-        for (int kb = 0; kb < nkb; ++kb) {
-            read_block(kb);
-            if (kb + 1 < nkb) copy_block(kb + 1);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            read_block();
+            if (kb + S - 1 < kb1) copy_block(kb + S - 1);
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             multiply();
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            zero_tail(kb + 1);
+            if (kb + 1 < kb1) landed(kb + 1);
             asm volatile("s_barrier" ::: "memory");
         }
         asm volatile("s_barrier" ::: "memory");
     } else {
-        if (nkb > 1) copy_block(1);
+        if (kb0 + S - 1 < kb1) copy_block(kb0 + S - 1);
         asm volatile("s_barrier" ::: "memory");
-        for (int kb = 0; kb < nkb; ++kb) {
-            read_block(kb);
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            zero_tail(kb + 1);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            read_block();
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (kb + 1 < kb1) landed(kb + 1);
             asm volatile("s_barrier" ::: "memory");
-            if (kb + 2 < nkb) copy_block(kb + 2);
+            if (kb + S < kb1) copy_block(kb + S);
             multiply();
             asm volatile("s_barrier" ::: "memory");
         }
     }
     __syncthreads();
-    store_tile<4, 2, GATED>(a, c, 0, t0 + 128 * wm, n0 + 32 * HN * wn, lane, (float *)(smem + wave * kWaveLds(2)), acc);
+    static_assert(8 * kWaveLds(2) <= S * kStage, "the epilogue fits the stages");
+    store_tile<TM, 2, GATED>(a, c, at.ks, t0 + 32 * TM * wm, n0 + 32 * HN * wn, lane, (float *)(smem + wave * kWaveLds(2)),
+                             acc);
 }
 
 constexpr int kMaxSplit = 8;
@@ -506,6 +518,12 @@ hipError_t launch_tile(const LinearArgs &a, const Cut &c, hipStream_t s)
                       S * (BM + BN) * 128, s);
 }
 
+template <bool BF16, bool GATED, int BM, int S>
+hipError_t launch_big(const LinearArgs &a, const Cut &c, hipStream_t s)
+{
+    return launch_cut((const void *)linear_big_kernel<BF16, GATED, BM, S>, a, c, 512, S * (BM + 256) * 128, s);
+}
+
 template <bool BF16>
 hipError_t launch_t(const LinearArgs &a, const Plan &p, hipStream_t s)
 {
@@ -520,11 +538,9 @@ hipError_t launch_t(const LinearArgs &a, const Plan &p, hipStream_t s)
         return a.wg ? launch_tile<BF16, 128, 128, 2, 2, true, 2>(a, p.c, s)
                     : launch_tile<BF16, 128, 128, 2, 2, false, 2>(a, p.c, s);
     case 3:
-        return a.wg ? launch_tile<BF16, 128, 256, 2, 4, true, 3>(a, p.c, s)
-                    : launch_tile<BF16, 128, 256, 2, 4, false, 3>(a, p.c, s);
+        return a.wg ? launch_big<BF16, true, 128, 3>(a, p.c, s) : launch_big<BF16, false, 128, 3>(a, p.c, s);
     }
-    return launch_cut(a.wg ? (const void *)linear_big_kernel<BF16, true> : (const void *)linear_big_kernel<BF16, false>, a,
-                      p.c, 512, 2 * 512 * 128, s);
+    return a.wg ? launch_big<BF16, true, 256, 2>(a, p.c, s) : launch_big<BF16, false, 256, 2>(a, p.c, s);
 }
 
 // Whether a call streams its weights past the tokens (linear_stream.hip) instead:
