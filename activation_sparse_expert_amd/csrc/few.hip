@@ -14,7 +14,7 @@
 // 64 experts of 2048 x 1408, top-6, and 2 shared ones: one token 32 us (139 MB in
 // kernels of 3.1 + 18.3 + 12.1 us, short streams), 32 tokens 220 us (1.1 GB, 5.0
 // TB/s: 4.6 + 10.4 + 125 + 86).  8 of 4096 x 14336, top-2, 4 tokens (5 or 6 of them
-// chosen): 293-351 us, gate/up at 6.1-6.3 TB/s.
+// chosen): 297-351 us, gate/up at 6.1-6.3 TB/s.
 // h is kept as the sum of two values of the 16-bit type (hi = its rounding,
 // lo = the rounding of the rest): the products with W^down are then good to
 // about 2^-17 (bf16) or 2^-22 (fp16) of h, and the rounding of y is the only one

@@ -8,16 +8,15 @@
 // instruction's A operand, so that a lane ends with four consecutive outputs of
 // a token and stores them together.
 //
-// Two kernels.  Large products take 256 x 256 tiles and 8 waves in two groups
-// a phase apart (linear_big_kernel).  The others take smaller tiles
+// Two kernels.  Large products take 256 x 256 or 128 x 256 tiles and 8 waves in two
+// groups a phase apart (linear_big_kernel), the others smaller tiles
 // (linear_tile_kernel); where those are few, K is split over workgroups, whose
 // fp32 products a second kernel adds in a fixed order before the epilogue.
 // plan() chooses by what each was measured to cost.
 // 4096 x 4096 x (2 x 14336), gated: 780-850 us, 1130-1230 TFLOP/s (MFMA busy 62%
 // of the cycles at the 1.75 GHz that the power limit leaves).  300 x 4096 x 4096:
-// 24 us in 128 x 256 tiles and 4 parts of K, and 5.6 us for their sum: a block of 64
-// k waits for its barrier, its fragments and its MFMAs in turn (1.0 us, of which
-// the MFMAs are 0.43).
+// 22 us in 128 x 256 tiles and 4 parts of K, and 5.6 us for their sum: 16 blocks of
+// 0.88 us, of which the MFMAs are 0.43, and the start and end of the tile.
 #include "linear_epilogue.hpp"
 
 namespace moeffn {
@@ -449,7 +448,8 @@ linear_join_kernel(LinearArgs a, int split)
 
 // The tiles that a call can take, and what a block of 64 k costs a compute unit, in
 // microseconds as measured: one workgroup alone on it, and two together where
-// two fit.  (Alone, a small tile waits: for its barrier, LDS and a chain of MFMAs.)
+// two fit.  (Alone, a small tile waits: for its barrier, LDS and a chain of MFMAs.
+// 128 x 256 costs 0.88 on a few units and 1.02 with all of them at work.)
 struct Tile {
     int bm, bn;                                     // tokens x weight rows
     double one, two;                                // two: 0 where one workgroup's LDS fills the unit
