@@ -18,8 +18,10 @@
 // h is kept as the sum of two values of the 16-bit type (hi = its rounding,
 // lo = the rounding of the rest): the products with W^down are then good to
 // about 2^-17 (bf16) or 2^-22 (fp16) of h, and the rounding of y is the only one
-// that shows.  hi and lo go through the matrix core as two tokens, which mostly fill
-// columns that would idle.  A column of the matrix core depends on its own token
+// that shows.  In fp16 lo is kept times 2^11 (kLoScale), since the rest of an h
+// below 2^-3 lies among fp16's subnormals, whose steps are coarser than 2^-22 of
+// it; of h down to 2^-14 lo then loses nothing.  hi and lo go through the matrix
+// core as two tokens, which mostly fill columns that would idle.  A column of the matrix core depends on its own token
 // alone, so infinities and NaN stay with the tokens whose experts hold them.
 #include "internal.hpp"
 #include "linear.hpp"
@@ -31,6 +33,11 @@ namespace moeffn {
 namespace {
 
 using st::floatx4;
+
+// What lo is kept times.  The rest of h is at most half a step of hi, 16, so that
+// its product stays below fp16's 65504; bf16 has fp32's exponents.
+template <bool BF16>
+constexpr float kLoScale = BF16 ? 1.f : 2048.f;
 
 // A listed expert, one 16-byte load: {expert or -1, its tokens as bits, first row,
 // down_cost of the experts before it}.  Its r-th token is the r-th set bit and has row
@@ -371,7 +378,7 @@ few_gateup_kernel(FewArgs a, int P, int slice)
         const uint16_t hi = st::to16<BF16>(h);
         const float back = st::from16<BF16>(hi);
         // an infinite or NaN h stands in hi alone
-        const uint16_t lo = fabsf(back) < INFINITY ? st::to16<BF16>(h - back) : (uint16_t)0;
+        const uint16_t lo = fabsf(back) < INFINITY ? st::to16<BF16>((h - back) * kLoScale<BF16>) : (uint16_t)0;
         uint16_t *dst = a.h + (size_t)(off + t) * 2 * a.f + ch;
         dst[0] = hi;
         dst[a.f] = lo;
@@ -403,7 +410,7 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
         const int v = min(8 * i + r, 2 * n - 1);
         src[2 * NM + i] = a.h + ((size_t)(off + (v < n ? v : v - n)) * 2 + (v < n ? 0 : 1)) * a.f + k;
     }
-    // this lane's columns: whether hi (0) or lo (1), their router weight and place in y
+    // this lane's columns: whether hi (0) or lo (1), their factor and place in y
     int at[R::kFrag], part[R::kFrag];
     float w[R::kFrag];
 #pragma unroll
@@ -412,6 +419,7 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
         part[j] = v < n ? 0 : v < 2 * n ? 1 : 2;
         at[j] = part[j] < 2 ? nth_bit((uint32_t)rec.y, first + t) * 16 * NM + 4 * (lane >> 4) : 0;
         w[j] = part[j] < 2 ? a.tab.wt[off + t] : 0.f;
+        if (part[j] == 1) w[j] *= 1.f / kLoScale<BF16>;
     }
     st::stream<BF16, NM, XR, D>(acc, ring, src, b1 - b0, b1 == blocks ? a.f - 64 * (blocks - 1) : 64, lane);
     // the hi columns first, then the lo ones: a token's two columns lie in two

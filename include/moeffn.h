@@ -346,7 +346,8 @@ moe_status moe_layer_forward(const moe_layer *L, const void *x, moe_dtype xdt, i
  * NULL.  Weights with infinities or NaN touch only the tokens sent to them.
  *   x [T][d] in xdt (== L->wdt), y [T][d] in ydt, residual [T][d] in ydt or
  *   NULL; residual and x may be y itself.  SiLU(g) u is kept to about 17 bits
- *   (bf16 layers) or 22 (fp16 layers, infinite beyond 65504), all sums in fp32.
+ *   (bf16 layers) or 22 (fp16 layers; absolutely to 2^-36 where it is below 2^-14,
+ *   infinite beyond 65504), all sums in fp32.
  *   Bit-reproducible for the same call; the order of a token's sums may depend
  *   on which experts the call's other tokens chose.
  * trace as moe_layer_forward's for the dense path (no masks, bits or nnz).
