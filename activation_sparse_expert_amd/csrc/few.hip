@@ -423,7 +423,9 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
     }
     st::stream<BF16, NM, XR, D>(acc, ring, src, b1 - b0, b1 == blocks ? a.f - 64 * (blocks - 1) : 64, lane);
     // the hi columns first, then the lo ones: a token's two columns lie in two
-    // lanes, whose sums must not be read before the other's are written
+    // lanes, whose sums must not be read before the other's are written.  Where an
+    // infinite weight has made a sum infinite (or NaN) it stays so: lo times that
+    // weight may be an infinity of the other sign, or 0 times it, a NaN.
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -432,7 +434,10 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
 #pragma unroll
                 for (int m = 0; m < NM; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[at[j] + 16 * m + i] += w[j] * acc[m][j][i];
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = y[at[j] + 16 * m + i];
+                        if (h == 0 || fabsf(v) < INFINITY) y[at[j] + 16 * m + i] = v + w[j] * acc[m][j][i];
+                    }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }

@@ -343,7 +343,8 @@ moe_status moe_layer_forward(const moe_layer *L, const void *x, moe_dtype xdt, i
  * Of L it reads d, f (both multiples of 8), n_routed, n_shared, top_k,
  * renormalize, wdt, the router, gate_t, up_dense and down_dense, which all have
  * to be there; the INT2 codes, `down` and the thresholds are not read and may be
- * NULL.  Weights with infinities or NaN touch only the tokens sent to them.
+ * NULL.  Weights with infinities or NaN touch only the tokens sent to them, and give
+ * those what the formula gives (in fp16 layers with 0 for a SiLU(g) u below 2^-25).
  *   x [T][d] in xdt (== L->wdt), y [T][d] in ydt, residual [T][d] in ydt or
  *   NULL; residual and x may be y itself.  SiLU(g) u is kept to about 17 bits
  *   (bf16 layers) or 22 (fp16 layers; absolutely to 2^-36 where it is below 2^-14,

@@ -72,3 +72,31 @@ def test_two_parts_of_h_at_every_scale(T, dt):
         y = moe.layer_forward_few(L, x)
         bound = h.abs() * (2.0 ** (-2 * BITS[dt]) + (2 * g.abs() + 10) * U) + (2.0 ** -36 if dt == "f16" else 2.0 ** -126)
         off(y, h, bound, f"T={T} {dt} scale {scale}")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T", [1, 3, 8, 13, 30])
+@pytest.mark.parametrize("own", [True, False])
+def test_infinite_down_weights_give_what_the_formula_gives(T, dt, own):
+    """An infinity of W^down times a finite h other than 0 is an infinity of the
+    product's sign, whatever the parts that h is kept in; the other outputs are as
+    without it, and two infinities of opposite sign make a NaN."""
+    f = 136
+    L, x, h, g = reading(T, f, DT[dt], 1.0, 3 + T)
+    out = DT[dt] if own else torch.float32
+    clean = moe.layer_forward_few(L, x, out_dtype=out)
+    assert float(h.abs().min()) > 2.0 ** -25            # the first part of none is 0 (fp16's step is 2^-24)
+    inf = float("inf")
+    L.down_dense[0, 5, 77] = inf
+    L.down_dense[0, 130, 3] = -inf
+    L.down_dense[0, 40, 7] = inf
+    L.down_dense[0, 40, 100] = inf
+    y = moe.layer_forward_few(L, x, out_dtype=out)
+    want = clean.double()
+    want[:, 5] = h[:, 77].sign() * inf
+    want[:, 130] = h[:, 3].sign() * -inf
+    a, b = h[:, 7].sign() * inf, h[:, 100].sign() * inf
+    want[:, 40] = a + b
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    fin = ~torch.isnan(want)
+    assert torch.equal(y.double()[fin], want[fin])
