@@ -446,7 +446,7 @@ size_t few_ws_bytes(int T, int d, int f, int E, int k, int S, FewWs *out, void *
 {
     const size_t rows = (size_t)T * (k + S), amax = few_amax(T, E, k, S);
     const size_t parts = few_parts(T, d, f, E, k, S);
-    const size_t size[7] = {(size_t)T * E * 4, 4, (amax + 1) * 16, rows * 4, rows * f * 4, (size_t)(d + 15) / 16 * 4,
+    const size_t size[7] = {(size_t)T * E * 4, 4, (amax + 1) * 16, rows * 4, rows * f * 2 * kFewTerms, (size_t)(d + 15) / 16 * 4,
                             parts * T * d * 4};
     size_t off[7], o = 0;
     for (int i = 0; i < 7; ++i) {

@@ -15,18 +15,20 @@
 // kernels of 3.1 + 18.3 + 12.1 us, short streams), 32 tokens 220 us (1.1 GB, 5.0
 // TB/s: 4.6 + 10.4 + 125 + 86).  8 of 4096 x 14336, top-2, 4 tokens (5 or 6 of them
 // chosen): 297-351 us, gate/up at 6.1-6.3 TB/s.
-// h is kept as the sum of two values of the 16-bit type (hi = its rounding,
-// lo = the rounding of the rest): the products with W^down are then good to
-// about 2^-17 (bf16) or 2^-22 (fp16) of h, and the rounding of y is the only one
-// that shows.  In fp16 lo is kept times 2^11 (kLoScale), since the rest of an h
-// below 2^-3 lies among fp16's subnormals, whose steps are coarser than 2^-22 of
-// it; of h down to 2^-14 lo then loses nothing.  hi and lo go through the matrix
-// core as two tokens, which mostly fill columns that would idle.  A column of the matrix core depends on its own token
+// h is kept as a sum of terms of the 16-bit type, each the rounding of what those
+// before it leave: three, which hold the 24 bits of fp32 (two bf16 terms would hold 17,
+// and turn one rounding of a bf16 y in a thousand), or two where both the type and y are
+// fp16: 22 bits, of which y shows 11.  In fp16 the second is kept times 2^11 and the third times
+// 2^22 (kTermScale), since the rest of an h below 2^-3 lies among fp16's subnormals,
+// whose steps are coarser than 2^-22 of it; of h down to 2^-14 lo then loses nothing.
+// The terms go through the matrix core as tokens of their own, which mostly fill
+// columns that would idle.  A column of the matrix core depends on its own token
 // alone, so infinities and NaN stay with the tokens whose experts hold them.
 #include "internal.hpp"
 #include "linear.hpp"
 #include "mfma_stream.hpp"
 #include "route_common.hpp"
+#include <type_traits>
 
 namespace moeffn {
 
@@ -34,10 +36,11 @@ namespace {
 
 using st::floatx4;
 
-// What lo is kept times.  The rest of h is at most half a step of hi, 16, so that
-// its product stays below fp16's 65504; bf16 has fp32's exponents.
+// What each term of h is kept times, over the one before.  The rest of a term is at
+// most half a step of it, 16, so that its product stays below fp16's 65504; bf16
+// has fp32's exponents.
 template <bool BF16>
-constexpr float kLoScale = BF16 ? 1.f : 2048.f;
+constexpr float kTermScale = BF16 ? 1.f : 2048.f;
 
 // A listed expert, one 16-byte load: {expert or -1, its tokens as bits, first row,
 // down_cost of the experts before it}.  Its r-th token is the r-th set bit and has row
@@ -48,12 +51,19 @@ __device__ __forceinline__ int nth_bit(uint32_t mask, int r)
     return __ffs(mask) - 1;
 }
 
-// What a block of an expert with n tokens costs in the down product, in half KB of
-// weights copied from HBM and, at half the price, of hi and lo rows from L2.
-__device__ __forceinline__ int down_cost(int n)
+// Rows of h that a pass of the down product over m <= 16 tokens copies
+__device__ __forceinline__ int down_rows(int m, int terms)
 {
-    auto pass = [](int m) { return m <= 4 ? 5 : m <= 8 ? 6 : 8; };
-    return n <= 16 ? pass(n) : 8 + pass(n - 16);
+    const int r = m * terms;
+    return r <= 8 ? 8 : r <= 16 ? 16 : terms == 2 ? 32 : r <= 24 ? 24 : 48;
+}
+
+// What a block of an expert with n tokens costs in the down product, in half KB of
+// weights copied from HBM and, at half the price, of rows of h from L2.
+__device__ __forceinline__ int down_cost(int n, int terms)
+{
+    auto pass = [=](int m) { return 4 + down_rows(m, terms) / 8; };
+    return n <= 16 ? pass(n) : pass(16) + pass(n - 16);
 }
 
 // The largest of the wave's 64 values, in every lane
@@ -202,7 +212,7 @@ __device__ void route(const FewArgs &a, int4 *rec, unsigned char *smem, bool exp
             const uint32_t m = e0 + lane < E ? em[e0 + lane] : 0u;
             const unsigned long long b = __ballot(m != 0u);
             // rows (at most 32 x 64 here) and costs, scanned together
-            const int c = __popc(m), v0 = c | (m ? down_cost(c) : 0) << 16;
+            const int c = __popc(m), v0 = c | (m ? down_cost(c, a.terms) : 0) << 16;
             int incl = v0;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
@@ -222,7 +232,7 @@ __device__ void route(const FewArgs &a, int4 *rec, unsigned char *smem, bool exp
         const uint32_t all = 0xFFFFFFFFu >> (32 - a.T);
         for (int i = na + lane; i <= a.amax; i += 64) {
             const int sh = i - na;
-            const int w = cost + min(sh, a.S) * down_cost(a.T);
+            const int w = cost + min(sh, a.S) * down_cost(a.T, a.terms);
             rec[i] = sh < a.S ? make_int4(E + sh, (int)all, rows + sh * a.T, w) : make_int4(-1, 0, 0, w);
         }
         if (lane == 0) *count = na + a.S;
@@ -285,13 +295,13 @@ __device__ __forceinline__ void gateup_wave(const FewArgs &a, unsigned char *rin
         for (int j = 0; j < R::kFrag; ++j) out[m][j] = acc[m][j];
 }
 
-// Bytes of a wave's ring in a kernel for at most xm token rows (hi and lo count
-// apart in the down product), and its depth where blocks hold xr of them: 3 or 4
+// Bytes of a wave's ring in a kernel for at most xm token rows (rows of h in the
+// down product), and its depth where blocks hold xr of them: 3 or 4
 // blocks at xm rows, as many as fit with fewer.
 constexpr int kUpRing(int xm) { return 3 * (4096 + 128 * xm); }
 constexpr int kUpDepth(int xm, int xr) { return kUpRing(xm) / (4096 + 128 * xr); }
-constexpr int kDownM(int xm) { return xm <= 16 ? 1 : 2; }  // groups of 16 columns
-constexpr int kDownRing(int xm) { return 4 * (2048 * kDownM(xm) + 128 * xm); }
+constexpr int kDownM(int xm) { return xm <= 24 ? 1 : 2; }  // groups of 16 columns
+constexpr int kDownRing(int xm) { return (xm <= 32 ? 4 : 3) * (2048 * kDownM(xm) + 128 * xm); }
 constexpr int kDownDepth(int xm, int xr) { return kDownRing(xm) / (2048 * kDownM(xm) + 128 * xr); }
 
 // Where the gate/up kernel has the list from
@@ -374,22 +384,23 @@ few_gateup_kernel(FewArgs a, int P, int slice)
         for (int z = 0; z < P; ++z)
 #pragma unroll
             for (int m = 0; m < 2; ++m) v[m] += red[((gg * P + z) * 2 + m) * NB * 256 + pos];
-        const float h = silu(v[0]) * v[1];
-        const uint16_t hi = st::to16<BF16>(h);
-        const float back = st::from16<BF16>(hi);
-        // an infinite or NaN h stands in hi alone
-        const uint16_t lo = fabsf(back) < INFINITY ? st::to16<BF16>((h - back) * kLoScale<BF16>) : (uint16_t)0;
-        uint16_t *dst = a.h + (size_t)(off + t) * 2 * a.f + ch;
-        dst[0] = hi;
-        dst[a.f] = lo;
+        float h = silu(v[0]) * v[1];
+        uint16_t *dst = a.h + (size_t)(off + t) * a.terms * a.f + ch;
+        for (int z = 0; z < a.terms; ++z) {
+            const uint16_t term = st::to16<BF16>(h);
+            const float back = st::from16<BF16>(term);
+            dst[(size_t)z * a.f] = term;
+            // an infinite or NaN h stands in the first term alone
+            h = fabsf(back) < INFINITY ? (h - back) * kTermScale<BF16> : 0.f;
+        }
     }
 }
 
 // One wave's share of one expert: 16 NM columns from col, blocks [b0, b1) of its
-// channels, tokens first .. first + n - 1 of the expert's; the 2 n columns of the matrix
-// core are hi, then lo of the n tokens.  The weighted sum goes into y [T][16 NM],
-// this wave's own LDS.
-template <bool BF16, int NM, int XR, int D>
+// channels, tokens first .. first + n - 1 of the expert's; the TERMS n columns of the
+// matrix core are the first terms of the n tokens' h, then the second, then the third.
+// The weighted sum goes into y [T][16 NM], this wave's own LDS.
+template <bool BF16, int TERMS, int NM, int XR, int D>
 __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring, float *y, int4 rec, int first, int n,
                                           int col, int b0, int b1, int blocks, int lane)
 {
@@ -407,30 +418,31 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
         src[i] = a.down_t + ((size_t)rec.x * a.d + min(col + 8 * i + r, a.d - 1)) * a.f + k;
 #pragma unroll
     for (int i = 0; i < R::kTok; ++i) {
-        const int v = min(8 * i + r, 2 * n - 1);
-        src[2 * NM + i] = a.h + ((size_t)(off + (v < n ? v : v - n)) * 2 + (v < n ? 0 : 1)) * a.f + k;
+        const int v = min(8 * i + r, TERMS * n - 1), z = v < n ? 0 : v < 2 * n ? 1 : 2;
+        src[2 * NM + i] = a.h + ((size_t)(off + v - z * n) * TERMS + z) * a.f + k;
     }
-    // this lane's columns: whether hi (0) or lo (1), their factor and place in y
-    int at[R::kFrag], part[R::kFrag];
+    // this lane's columns: their term (TERMS: none), factor and place in y
+    int at[R::kFrag], term[R::kFrag];
     float w[R::kFrag];
 #pragma unroll
     for (int j = 0; j < R::kFrag; ++j) {
-        const int v = 16 * j + (lane & 15), t = v < n ? v : v - n;
-        part[j] = v < n ? 0 : v < 2 * n ? 1 : 2;
-        at[j] = part[j] < 2 ? nth_bit((uint32_t)rec.y, first + t) * 16 * NM + 4 * (lane >> 4) : 0;
-        w[j] = part[j] < 2 ? a.tab.wt[off + t] : 0.f;
-        if (part[j] == 1) w[j] *= 1.f / kLoScale<BF16>;
+        const int v = 16 * j + (lane & 15), z = v < n ? 0 : v < 2 * n ? 1 : v < 3 * n ? 2 : 3, t = v - z * n;
+        constexpr float s = 1.f / kTermScale<BF16>;
+        term[j] = min(z, TERMS);
+        at[j] = z < TERMS ? nth_bit((uint32_t)rec.y, first + t) * 16 * NM + 4 * (lane >> 4) : 0;
+        w[j] = z < TERMS ? a.tab.wt[off + t] * (z == 0 ? 1.f : z == 1 ? s : s * s) : 0.f;
     }
     st::stream<BF16, NM, XR, D>(acc, ring, src, b1 - b0, b1 == blocks ? a.f - 64 * (blocks - 1) : 64, lane);
-    // the hi columns first, then the lo ones: a token's two columns lie in two
-    // lanes, whose sums must not be read before the other's are written.  Where an
-    // infinite weight has made a sum infinite (or NaN) it stays so: lo times that
-    // weight may be an infinity of the other sign, or 0 times it, a NaN.
+    // the columns of the first terms, then of the second, then of the third: those of
+    // a token lie in different lanes, whose sums must not be read before the
+    // others' are written.  Where an infinite weight has made a sum infinite (or NaN)
+    // it stays so: a later term times that weight may be an infinity of the other
+    // sign, or 0 times it, a NaN.
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < TERMS; ++h) {
 #pragma unroll
         for (int j = 0; j < R::kFrag; ++j)
-            if (part[j] == h)
+            if (term[j] == h)
 #pragma unroll
                 for (int m = 0; m < NM; ++m)
 #pragma unroll
@@ -442,11 +454,12 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
     }
 }
 
-// XM: hi and lo rows that a pass can have (2, 8, 16 or 32): an expert with more
-// than 16 tokens takes two passes over its weights.  Workgroup b takes columns
+// XM: rows of h that a pass can have (2, 8, 16 or 32 by two terms, 4, 16, 24 or 48
+// by three): an expert with more than 16 tokens takes two passes over its weights.
+// Workgroup b takes columns
 // C (b % nblk) .. and part b / nblk of `parts`; the waves of all parts take
 // equal shares of the blocks' costs, in the order of the list.
-template <bool BF16, int XM>
+template <bool BF16, int TERMS, int XM>
 __global__ void __launch_bounds__(256)
 few_down_kernel(FewArgs a, int parts)
 {
@@ -462,14 +475,14 @@ few_down_kernel(FewArgs a, int parts)
     const int nblk = (a.d + C - 1) / C, part = blockIdx.x / nblk, blk = blockIdx.x - part * nblk;
     const int n0 = C * blk;
     const int blocks = (a.f + 63) / 64, share = part * waves + wave, shares = parts * waves;
-    if constexpr (XM == 2) {
+    if constexpr (XM < 8) {
         // one token: every listed expert has it
         const long long total = (long long)a.amax * blocks;
         const int beg = (int)(total * share / shares), end = (int)(total * (share + 1) / shares);
         for (int s = beg; s < end;) {
             const int i = s / blocks, b0 = s - i * blocks, b1 = min(blocks, b0 + end - s);
             s += b1 - b0;
-            down_wave<BF16, NM, 2, kDownDepth(2, 2)>(a, ring, y, a.tab.rec[i], 0, 1, n0, b0, b1, blocks, lane);
+            down_wave<BF16, TERMS, NM, XM, kDownDepth(XM, XM)>(a, ring, y, a.tab.rec[i], 0, 1, n0, b0, b1, blocks, lane);
         }
     } else {
         // a list entry's w is the cost of the blocks of one column before it / blocks
@@ -481,7 +494,7 @@ few_down_kernel(FewArgs a, int parts)
             i += __popcll(__ballot(i0 + lane < n && (long long)a.tab.rec[i0 + min(lane, n - 1 - i0)].w * blocks <= beg));
         for (; i < n; ++i) {
             const int4 rec = a.tab.rec[i];
-            const int all = __popc((uint32_t)rec.y), cost = down_cost(all);
+            const int all = __popc((uint32_t)rec.y), cost = down_cost(all, TERMS);
             const long long at = (long long)rec.w * blocks;
             if (at >= end) break;
             // the blocks that begin within the share
@@ -490,11 +503,15 @@ few_down_kernel(FewArgs a, int parts)
             if (b0 >= b1) continue;
             for (int first = 0; first < all; first += 16) {
                 const int m = min(16, all - first);
-                if (XM == 8 || m <= 4)
-                    down_wave<BF16, NM, 8, kDownDepth(XM, 8)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
-                else if (XM == 16 || m <= 8)
-                    down_wave<BF16, NM, 16, kDownDepth(XM, 16)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
-                else down_wave<BF16, NM, 32, kDownDepth(XM, 32)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
+                const int rows = down_rows(m, TERMS);
+                auto pass = [&](auto xr) {
+                    constexpr int XR = decltype(xr)::value;
+                    down_wave<BF16, TERMS, NM, XR, kDownDepth(XM, XR)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
+                };
+                if (XM == 8 || rows == 8) pass(std::integral_constant<int, 8>());
+                else if (XM == 16 || rows == 16) pass(std::integral_constant<int, XM < 16 ? XM : 16>());
+                else if (XM == 24 || rows == 24) pass(std::integral_constant<int, XM < 24 ? XM : 24>());
+                else pass(std::integral_constant<int, XM>());
             }
         }
     }
@@ -576,18 +593,32 @@ hipError_t gateup_for(const FewArgs &a, int route, hipStream_t s)
     return a.T <= 16 ? gateup<BF16, 16, kFromList>(a, s) : gateup<BF16, 32, kFromList>(a, s);
 }
 
-template <bool BF16, int XM>
+template <bool BF16, int TERMS, int XM>
 hipError_t down(const FewArgs &a, hipStream_t s)
 {
     constexpr int W = 4;
     constexpr int C = 16 * kDownM(XM);
     const size_t lds = (size_t)W * (kDownRing(XM) + a.T * C * 4);
-    const hipError_t e = allow_lds((const void *)few_down_kernel<BF16, XM>, lds);
+    const hipError_t e = allow_lds((const void *)few_down_kernel<BF16, TERMS, XM>, lds);
     if (e != hipSuccess) return e;
     const int parts = few_parts(a.T, a.d, a.f, a.E, a.k, a.S);
-    hipLaunchKernelGGL((few_down_kernel<BF16, XM>), dim3((unsigned)((a.d + C - 1) / C * parts)), dim3(64 * W), lds, s,
+    hipLaunchKernelGGL((few_down_kernel<BF16, TERMS, XM>), dim3((unsigned)((a.d + C - 1) / C * parts)), dim3(64 * W), lds, s,
                        a, parts);
     return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t down_for(const FewArgs &a, hipStream_t s)
+{
+    if constexpr (!BF16)
+        if (a.terms == 2) {
+            if (a.T == 1) return down<BF16, 2, 2>(a, s);
+            if (a.T <= 4) return down<BF16, 2, 8>(a, s);
+            return a.T <= 8 ? down<BF16, 2, 16>(a, s) : down<BF16, 2, 32>(a, s);
+        }
+    if (a.T == 1) return down<BF16, 3, 4>(a, s);
+    if (a.T <= 5) return down<BF16, 3, 16>(a, s);
+    return a.T <= 8 ? down<BF16, 3, 24>(a, s) : down<BF16, 3, 48>(a, s);
 }
 
 bool args_ok(const FewArgs &a)
@@ -620,9 +651,15 @@ int few_parts(int T, int d, int f, int E, int k, int S)
     return p;
 }
 
-hipError_t launch_few(const FewArgs &a, hipStream_t s)
+// (measured, us, two terms and three: 32 tokens of 64 experts of 2048 x 1408, top-6, 197 and
+// 204, of which y twice as wide is a part; 4 tokens of 8 of 4096 x 14336 327 and 333)
+static int few_terms(int bf16, int ydt) { return !bf16 && ydt == 0 ? 2 : kFewTerms; }
+
+hipError_t launch_few(const FewArgs &args, hipStream_t s)
 {
-    if (!args_ok(a)) return hipErrorInvalidValue;
+    if (!args_ok(args)) return hipErrorInvalidValue;
+    FewArgs a = args;
+    a.terms = few_terms(a.bf16, a.ydt);
     // Who works the router out.  Every gate/up workgroup for itself where that
     // takes less than a kernel more: all of it up to 32768 products, for one token the choice
     // alone; both only in layers of about one round of workgroups (1024), since each pays.
@@ -652,10 +689,7 @@ hipError_t launch_few(const FewArgs &a, hipStream_t s)
     }
     e = a.bf16 ? gateup_for<true>(a, route, s) : gateup_for<false>(a, route, s);
     if (e != hipSuccess) return e;
-    if (a.T == 1) return a.bf16 ? down<true, 2>(a, s) : down<false, 2>(a, s);
-    if (a.T <= 4) return a.bf16 ? down<true, 8>(a, s) : down<false, 8>(a, s);
-    if (a.T <= 8) return a.bf16 ? down<true, 16>(a, s) : down<false, 16>(a, s);
-    return a.bf16 ? down<true, 32>(a, s) : down<false, 32>(a, s);
+    return a.bf16 ? down_for<true>(a, s) : down_for<false>(a, s);
 }
 
 }  // namespace moeffn

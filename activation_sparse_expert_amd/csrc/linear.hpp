@@ -50,7 +50,8 @@ struct FewArgs {
     float *lg;                          // [T][E] logits (workspace)
     FewTab tab;
     int amax;                           // bound of the listed experts: min(E, T k) + S
-    uint16_t *h;                        // [T (k + S)][hi, lo][f] (workspace)
+    int terms;                          // that h is kept in (launch_few sets it)
+    uint16_t *h;                        // [T (k + S)][terms][f] (workspace)
     float *part;                        // [few_parts][T][d] (workspace)
     const void *r;                      // [T][d] or null
     void *y;                            // [T][d]
@@ -61,6 +62,7 @@ struct FewArgs {
 };
 
 constexpr int kFewTokens = 32;
+constexpr int kFewTerms = 3;            // the most
 constexpr int kFewRows = 2048;          // T (k + S)
 int few_amax(int T, int E, int k, int S);
 int few_parts(int T, int d, int f, int E, int k, int S);

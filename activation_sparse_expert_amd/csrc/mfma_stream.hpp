@@ -74,7 +74,7 @@ __device__ __forceinline__ void wait_copies()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// XR: token rows of a block (1, 2 or a multiple of 8)
+// XR: token rows of a block (1, 2, 4 or a multiple of 8)
 template <int NM, int XR>
 struct Ring {
     static constexpr int kTok = (XR + 7) / 8;           // copy instructions of tokens
@@ -102,7 +102,7 @@ __device__ __forceinline__ void stream(typename Ring<NM, XR>::Acc &acc, unsigned
                                        typename Ring<NM, XR>::Src &src, int nb, int kl, int lane)
 {
     using R = Ring<NM, XR>;
-    static_assert(XR == 1 || XR == 2 || XR % 8 == 0, "token rows");
+    static_assert(XR == 1 || XR == 2 || XR == 4 || XR % 8 == 0, "token rows");
     const int li = lane & 15, q = lane >> 4;
     const int kc = copy_k(lane);
     int put = 0, get = 0, issued = 0;
@@ -131,7 +131,7 @@ __device__ __forceinline__ void stream(typename Ring<NM, XR>::Acc &acc, unsigned
             for (int j = 0; j < R::kFrag; ++j) {
                 int xt = at;
                 if (XR == 1) xt = 16 * c;
-                else if (XR == 2) xt = (li & 1) * 128 + 16 * (c ^ (li & 1));
+                else if (XR < 8) xt = (li & (XR - 1)) * 128 + 16 * (c ^ (li & (XR - 1)));
                 else if (16 * j + 8 == XR) xt = at & 1023;
                 x[j] = *(const uint4 *)(d + 2048 * (NM + j) + xt);
             }

@@ -346,10 +346,10 @@ moe_status moe_layer_forward(const moe_layer *L, const void *x, moe_dtype xdt, i
  * NULL.  Weights with infinities or NaN touch only the tokens sent to them, and give
  * those what the formula gives (in fp16 layers with 0 for a SiLU(g) u below 2^-25).
  *   x [T][d] in xdt (== L->wdt), y [T][d] in ydt, residual [T][d] in ydt or
- *   NULL; residual and x may be y itself.  SiLU(g) u is kept to about 17 bits
- *   (bf16 layers) or 22 (fp16 layers; absolutely to 2^-36 where it is below 2^-14,
- *   infinite beyond 65504), all sums in fp32.
- *   Bit-reproducible for the same call; the order of a token's sums may depend
+ *   NULL; residual and x may be y itself.  SiLU(g) u is kept to fp32's 24 bits
+ *   (fp16 layers: to 2^-47 where it is below 2^-24), in fp16 layers whose y is fp16 to 22
+ *   (to 2^-36 where it is below 2^-14); in fp16 layers it is infinite beyond 65504.
+ *   All sums are fp32.  Bit-reproducible for the same call; the order of a token's sums may depend
  *   on which experts the call's other tokens chose.
  * trace as moe_layer_forward's for the dense path (no masks, bits or nnz).
  * Limits: T (k + S) <= 2048, E <= 1024 (else MOE_ERR_UNSUPPORTED).

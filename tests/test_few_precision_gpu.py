@@ -9,8 +9,8 @@ at most (2 |g| + 2) u (its argument is rounded twice, in g log2 e), 1 + exp(-g),
 the quotient and the product by u by one rounding each, the sums of h's parts
 and of the waves by one each: (2 |g| + 10) u.  A part of h has the 16-bit type's
 P = 11 (fp16) or 8 (bf16) bits, so its rounding leaves at most 2^-P of what it
-rounds; in fp16 a part is at least half a step of 2^-24 exact, and the second
-part is kept times 2^11."""
+rounds; in fp16 a part is at least half a step of 2^-24 exact, and the second and
+third part are kept times 2^11 and 2^22."""
 import pytest
 import torch
 
@@ -72,6 +72,35 @@ def test_two_parts_of_h_at_every_scale(T, dt):
         y = moe.layer_forward_few(L, x)
         bound = h.abs() * (2.0 ** (-2 * BITS[dt]) + (2 * g.abs() + 10) * U) + (2.0 ** -36 if dt == "f16" else 2.0 ** -126)
         off(y, h, bound, f"T={T} {dt} scale {scale}")
+
+
+@pytest.mark.parametrize("dt,out", [("f16", torch.float32), ("bf16", torch.float32), ("bf16", torch.float16),
+                                    ("f16", torch.bfloat16)])
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 6, 8, 9, 10, 13, 16, 17, 27, 32])
+def test_outputs_of_another_type_lose_nothing_of_h(T, dt, out):
+    """h has 24 bits, as an fp32 h has (in fp16 2^-47 for the smallest)."""
+    for i, scale in enumerate(SCALES):
+        L, x, h, g = reading(T, 264, DT[dt], scale, 20 * T + i)
+        y = moe.layer_forward_few(L, x, out_dtype=out)
+        bound = h.abs() * ((2 * g.abs() + 11) * U) + (2.0 ** -47 if dt == "f16" else 2.0 ** -126)
+        if out != torch.float32:
+            fi = torch.finfo(out)
+            bound = bound + h.abs() * fi.eps / 2 * 1.001 + fi.smallest_normal * fi.eps / 2
+        off(y, h, bound, f"T={T} {dt} -> {out} scale {scale}")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T", [1, 4, 8, 13, 32])
+def test_y_of_the_own_type_is_rounded_once(T, dt):
+    """y is h rounded to the layer's type, up to the 24 bits (fp16: 22) that h has: off by
+    half a step of y and no more than those."""
+    for i, scale in enumerate([2.0 ** -3, 1.0, 4.0]):
+        L, x, h, g = reading(T, 264, DT[dt], scale, 30 * T + i)
+        y = moe.layer_forward_few(L, x, out_dtype=DT[dt])
+        low = -14 if dt == "f16" else -126               # the exponent of the smallest normal value
+        step = torch.ldexp(torch.ones_like(h), torch.frexp(h.abs())[1].clamp(min=low + 1) - BITS[dt])
+        kept = h.abs() * 2.0 ** -22 + 2.0 ** -36 if dt == "f16" else 2.0 ** -126
+        off(y, h, step / 2 + kept + h.abs() * (2 * g.abs() + 11) * U, f"T={T} {dt} scale {scale}")
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
