@@ -19,7 +19,9 @@ template <int ACT>
 __device__ __forceinline__ float activate(float v)
 {
     if constexpr (ACT == 1) return v != v ? v : fmaxf(v, 0.f);                      // ReLU (a NaN stays one)
-    else if constexpr (ACT == 2) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));    // GELU
+    // GELU: 1 + erf z = erfc(-z), which does not cancel where v is negative (at -5
+    // the sum is off by a tenth of itself, several steps of a bf16 y)
+    else if constexpr (ACT == 2) return 0.5f * v * erfcf(v * -0.70710678118654752f);
     // GELU, tanh form: 0.5 v (1 + tanh z) = v sigmoid(2 z)
     else if constexpr (ACT == 3) return gate_by(v, 1.59576912160573072f * (v + 0.044715f * v * v * v));
     else if constexpr (ACT == 4) return gate_by(v, v);                              // SiLU

@@ -365,7 +365,8 @@ moe_status moe_layer_forward_few(const moe_layer *L, const void *x, moe_dtype xd
  * of the product (the dense FFN layers and projections around the MoE layers):
  *   y = residual + act(x W^T + bias), or with L->w_gate
  *   y = residual + act(x Wg^T + bias_gate) (.) (x W^T + bias)
- * with fp32 sums and one rounding, to ydt.
+ * with fp32 sums and one rounding, to ydt.  Activations are evaluated in fp32, to a few
+ * units of their value times 1 + v^2 (SiLU: 1 + |v|), v their argument.
  *   x [T][k] in xdt (== L->wdt), y [T][n] in ydt, residual [T][n] in ydt or
  *   NULL; rows at x_stride, y_stride and residual_stride elements (at least the
  *   row's length; x_stride a multiple of 8).  residual may be y itself, at
