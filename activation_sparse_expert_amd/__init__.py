@@ -32,7 +32,7 @@ EXPORTED = ["moe_route_topk", "moe_expert_forward_sparse", "moe_layer_forward",
             "moe_build_sources_sha256", "moe_expert_forward_sparse_noalloc",
             "moe_noalloc_scratch_bytes", "moe_materialize_up", "moe_transpose_down",
             "moe_auto_dense_min", "moe_mixed_dense_min", "moe_layer_forward_few",
-            "moe_linear_forward"]
+            "moe_linear_forward", "moe_linear_plan"]
 
 
 class MoeError(RuntimeError):
@@ -133,6 +133,8 @@ def lib():
         L.moe_linear_forward.restype = I
         L.moe_linear_forward.argtypes = [C.POINTER(LinearDesc), P, I, C.c_longlong, I, P,
                                          C.c_longlong, P, I, C.c_longlong, P, Z, P]
+        L.moe_linear_plan.restype = I
+        L.moe_linear_plan.argtypes = [I, I, I, I, C.POINTER(I), C.POINTER(I)]
         _lib = L
     return _lib
 
@@ -519,6 +521,16 @@ def linear_forward(linear: Linear, x, *, residual=None, y=None, out_dtype=None, 
     _call(torch, device, "moe_linear_forward", lib().moe_linear_forward, C.byref(linear.desc()), xp,
           _dt(x), xs, T, rp, rs, yp, _dt(y), ys, wp, wb)
     return y
+
+
+def linear_plan(T: int, k: int, n: int, gated: bool = False):
+    """How linear_forward cuts a call of these sizes: ((tokens, weight rows) of a tile,
+    parts of k), or (None, 0) where it streams the weights past the tokens."""
+    tokens, rows = C.c_int(), C.c_int()
+    parts = lib().moe_linear_plan(T, k, n, int(gated), C.byref(tokens), C.byref(rows))
+    if parts < 0:
+        raise ValueError(f"the linear layer does not take T = {T}, k = {k}, n = {n}")
+    return ((tokens.value, rows.value) if parts else None), parts
 
 
 def calibrate_threshold(v, q: float, *, out=None, ws=None):

@@ -1023,6 +1023,15 @@ moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt,
     return hip_status(launch_linear(a, s));
 }
 
+int moe_linear_plan(int T, int k, int n, int gated, int *tokens, int *rows)
+{
+    int bm = 0, bn = 0, parts = -1;
+    if (linear_size_ok(T, k, n)) parts = linear_parts(T, k, n, gated != 0, &bm, &bn);
+    if (tokens) *tokens = bm;
+    if (rows) *rows = bn;
+    return parts;
+}
+
 moe_status moe_pack_up_int2(const void *w_up_t, moe_dtype dt, int d, int f, uint8_t *up_q,
                             uint16_t *up_sz, void *stream)
 {

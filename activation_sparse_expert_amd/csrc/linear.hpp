@@ -25,6 +25,8 @@ struct LinearArgs {
 
 hipError_t launch_linear(const LinearArgs &a, hipStream_t s);
 hipError_t launch_linear_stream(const LinearArgs &a, hipStream_t s);    // no workspace
+// The parts of K of a call (0: streamed) and its tile
+int linear_parts(int T, int K, int N, bool gated, int *bm, int *bn);
 size_t linear_ws_bytes(int T, int K, int N);            // enough for the plain and the gated call
 
 // The few-token MoE layer: the experts of a call and their tokens, made from the

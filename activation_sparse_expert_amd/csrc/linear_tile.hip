@@ -555,6 +555,15 @@ bool streams(int T, int K, int N)
 
 }  // namespace
 
+int linear_parts(int T, int K, int N, bool gated, int *bm, int *bn)
+{
+    if (streams(T, K, N)) return 0;
+    const Plan p = plan(T, K, N, gated);
+    *bm = kTiles[p.tile].bm;
+    *bn = kTiles[p.tile].bn;
+    return p.c.split;
+}
+
 size_t linear_ws_bytes(int T, int K, int N)
 {
     if (streams(T, K, N)) return 0;

@@ -384,6 +384,14 @@ moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt,
                               void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * How moe_linear_forward cuts a call of these sizes (x_stride up to 2^21): into how many
+ * parts of k, in tiles of *tokens x *rows (of W, or of W and W^gate together); 0 where
+ * the weights are streamed past the tokens instead, -1 for sizes that it refuses.
+ * Either pointer may be NULL.
+ */
+int moe_linear_plan(int T, int k, int n, int gated, int *tokens, int *rows);
+
+/*
  * MOE_PATH_AUTO's choice for a call of T tokens on this layer (without mask
  * exports, dense weights 16-byte aligned): 1 when the call takes the dense
  * path (every expert with tokens), 0 when it takes the sparse path.  Host
