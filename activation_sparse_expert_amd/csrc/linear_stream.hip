@@ -7,6 +7,8 @@
 // Bound by HBM: 1 x 4096 x 28672 (gated) 38 us, 6.2 TB/s; 16 x 14336 x 4096 24 us, 4.8 TB/s.
 #include "linear_epilogue.hpp"
 
+#include <algorithm>
+
 namespace moeffn {
 
 namespace {
@@ -130,7 +132,21 @@ hipError_t launch_t(const LinearArgs &a, hipStream_t s)
 hipError_t launch_linear_stream(const LinearArgs &a, hipStream_t s)
 {
     if (a.T < 1 || a.K < 8 || a.K % 8 != 0 || a.N < 1) return hipErrorInvalidValue;
-    return a.bf16 ? launch_t<true>(a, s) : launch_t<false>(a, s);
+    // A launch may have at most 2^32 - 1 threads, here 512 a workgroup and one workgroup
+    // for 16 outputs of 32 tokens at the most: more tokens go in runs.
+    const long long sets = ((long long)a.N + 127) / 128 * 8;
+    const int run = 32 * (int)std::max(1ll, (1ll << 22) / sets);
+    const size_t ye = a.ydt == 2 ? 4 : 2;
+    LinearArgs b = a;
+    for (int t = 0; t < a.T; t += run) {
+        b.T = std::min(run, a.T - t);
+        b.x = a.x + (size_t)t * a.xs;
+        b.y = (char *)a.y + ye * t * a.ys;
+        if (a.r) b.r = (const char *)a.r + ye * t * a.rs;
+        const hipError_t e = a.bf16 ? launch_t<true>(b, s) : launch_t<false>(b, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace moeffn
