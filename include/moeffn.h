@@ -352,7 +352,8 @@ moe_status moe_layer_forward(const moe_layer *L, const void *x, moe_dtype xdt, i
  *   All sums are fp32.  Bit-reproducible for the same call; the order of a token's sums may depend
  *   on which experts the call's other tokens chose.
  * trace as moe_layer_forward's for the dense path (no masks, bits or nnz).
- * Limits: T (k + S) <= 2048, E <= 1024 (else MOE_ERR_UNSUPPORTED).
+ * Limits: T <= 32, d <= 16384, T (k + S) <= 2048 (else MOE_ERR_UNSUPPORTED); E <= 1024,
+ * k <= E (else MOE_ERR_INVALID_ARG).
  * Workspace: moe_workspace_size(MOE_OP_LAYER_FEW, T, d, f, E, k, S) bytes.
  */
 moe_status moe_layer_forward_few(const moe_layer *L, const void *x, moe_dtype xdt, int T,
@@ -371,8 +372,8 @@ moe_status moe_layer_forward_few(const moe_layer *L, const void *x, moe_dtype xd
  *   NULL; rows at x_stride, y_stride and residual_stride elements (at least the
  *   row's length; x_stride a multiple of 8).  residual may be y itself, at
  *   the same stride; y must not overlap x or the weights otherwise.
- * Limits: 1 <= T <= 65536; k a multiple of 8 up to 2^20, n up to 2^24 (else
- * MOE_ERR_UNSUPPORTED); x and the weights 16-byte aligned.  The order of the
+ * Limits: 1 <= T <= 65536 (else MOE_ERR_INVALID_ARG); k a multiple of 8 up to 2^20, n up
+ * to 2^24 (else MOE_ERR_UNSUPPORTED); x and the weights 16-byte aligned.  The order of the
  * sums depends on T, n, k, whether the layer is gated and (past 2^21) x_stride,
  * never on values or addresses: outputs are bit-reproducible.
  * Workspace: moe_workspace_size(MOE_OP_LINEAR, T, k, n, 0, 0, 0) bytes, gated or

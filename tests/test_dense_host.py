@@ -100,3 +100,22 @@ def test_binding_checks_before_the_library():
         moe.Linear(w, act="tanh").desc()
     with pytest.raises(ValueError, match=r"\[T\]\[d\]"):
         moe.layer_forward_few(None, torch.zeros(8, dtype=torch.float16))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=32, d=16384, top_k=2, ws_bytes=0), -4), (dict(T=32, d=16392, top_k=2), -2), (dict(T=33), -2),
+    (dict(T=32, top_k=62, ws_bytes=0), -4), (dict(T=32, top_k=63), -2),
+    (dict(n_routed=1024, ws_bytes=0), -4), (dict(n_routed=1025), -1), (dict(n_routed=4, top_k=5), -1),
+])
+def test_few_limits_are_the_documented_ones(kw, code):
+    """Both sides of each limit; on the near side the workspace is what is missing."""
+    assert _few(**kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=65536, ws=FAKE + 8), -3), (dict(T=65537), -1), (dict(k=1 << 20, T=40, ws_bytes=0), -4),
+    (dict(k=(1 << 20) + 8), -2), (dict(n=(1 << 24) + 1), -2),
+])
+def test_linear_limits_are_the_documented_ones(kw, code):
+    """Both sides of each limit; on the near side it is the workspace that is refused."""
+    assert _linear(**kw) == code
