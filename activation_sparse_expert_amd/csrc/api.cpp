@@ -1009,6 +1009,7 @@ moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt,
     const size_t need = up(linear_ws_bytes(T, k, n));
     if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return MOE_ERR_ALIGNMENT;
+    if (x == y) return MOE_ERR_INVALID_ARG;             // other workgroups may not have read it
     LinearArgs a{};
     a.T = T; a.K = k; a.N = n;
     a.bf16 = L->wdt == MOE_BF16 ? 1 : 0;

@@ -371,7 +371,8 @@ moe_status moe_layer_forward_few(const moe_layer *L, const void *x, moe_dtype xd
  *   x [T][k] in xdt (== L->wdt), y [T][n] in ydt, residual [T][n] in ydt or
  *   NULL; rows at x_stride, y_stride and residual_stride elements (at least the
  *   row's length; x_stride a multiple of 8).  residual may be y itself, at
- *   the same stride; y must not overlap x or the weights otherwise.
+ *   the same stride; y must not overlap x (x == y: MOE_ERR_INVALID_ARG) or the
+ *   weights otherwise.
  * Limits: 1 <= T <= 65536 (else MOE_ERR_INVALID_ARG); k a multiple of 8 up to 2^20, n up
  * to 2^24 (else MOE_ERR_UNSUPPORTED); x and the weights 16-byte aligned.  The order of the
  * sums depends on T, n, k, whether the layer is gated and (past 2^21) x_stride,

@@ -119,3 +119,8 @@ def test_few_limits_are_the_documented_ones(kw, code):
 def test_linear_limits_are_the_documented_ones(kw, code):
     """Both sides of each limit; on the near side it is the workspace that is refused."""
     assert _linear(**kw) == code
+
+
+def test_linear_refuses_its_input_as_output():
+    assert _linear(T=1, n=256, k=256, ws=None, ws_bytes=0) == -1
+    assert _linear(T=40, n=256, k=256) == -1
