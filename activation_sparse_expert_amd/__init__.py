@@ -431,8 +431,8 @@ def layer_forward_few(layer: Layer, x, *, residual=None, y=None, out_dtype=None,
     T, d = x.shape
     E, S, f, k = layer.E, layer.S, layer.f, layer.k
     gate, up, down = layer.gate_t, layer.up_dense, layer.down_dense
-    if up is None or down is None:
-        raise ValueError("the layer needs up_dense and down_dense")
+    if layer.router_w is None or gate is None or up is None or down is None:
+        raise ValueError("the layer needs router_w, gate_t, up_dense and down_dense")
     if d != layer.d:
         raise ValueError(f"x has {d} columns, the layer d = {layer.d}")
     wdt = gate.dtype
