@@ -297,12 +297,16 @@ __device__ __forceinline__ void gateup_wave(const FewArgs &a, unsigned char *rin
 
 // Bytes of a wave's ring in a kernel for at most xm token rows (rows of h in the
 // down product), and its depth where blocks hold xr of them: 3 or 4
-// blocks at xm rows, as many as fit with fewer.
+// blocks at xm rows, as many as fit with fewer.  (Three terms take 3, so that as
+// many workgroups share a compute unit as with two.)
 constexpr int kUpRing(int xm) { return 3 * (4096 + 128 * xm); }
 constexpr int kUpDepth(int xm, int xr) { return kUpRing(xm) / (4096 + 128 * xr); }
 constexpr int kDownM(int xm) { return xm <= 24 ? 1 : 2; }  // groups of 16 columns
-constexpr int kDownRing(int xm) { return (xm <= 32 ? 4 : 3) * (2048 * kDownM(xm) + 128 * xm); }
-constexpr int kDownDepth(int xm, int xr) { return kDownRing(xm) / (2048 * kDownM(xm) + 128 * xr); }
+constexpr int kDownRing(int terms, int xm)
+{
+    return (terms == 3 && xm > 8 ? 3 : 4) * (2048 * kDownM(xm) + 128 * xm);
+}
+constexpr int kDownDepth(int terms, int xm, int xr) { return kDownRing(terms, xm) / (2048 * kDownM(xm) + 128 * xr); }
 
 // Where the gate/up kernel has the list from
 enum { kFromList = 0, kFromLogits = 1, kFromRouter = 2 };
@@ -431,6 +435,9 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
         term[j] = min(z, TERMS);
         at[j] = z < TERMS ? nth_bit((uint32_t)rec.y, first + t) * 16 * NM + 4 * (lane >> 4) : 0;
         w[j] = z < TERMS ? a.tab.wt[off + t] * (z == 0 ? 1.f : z == 1 ? s : s * s) : 0.f;
+        // arrived here: else the compiler waits for it inside the stream, and for the
+        // copies with it (13 tokens, 8 experts of 4096 x 14336: 150 us against 210)
+        asm volatile("" : "+v"(w[j]));
     }
     st::stream<BF16, NM, XR, D>(acc, ring, src, b1 - b0, b1 == blocks ? a.f - 64 * (blocks - 1) : 64, lane);
     // the columns of the first terms, then of the second, then of the third: those of
@@ -454,7 +461,7 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
     }
 }
 
-// XM: rows of h that a pass can have (2, 8, 16 or 32 by two terms, 4, 16, 24 or 48
+// XM: rows of h that a pass can have (2, 8, 16 or 32 by two terms, 4, 8, 16, 24 or 48
 // by three): an expert with more than 16 tokens takes two passes over its weights.
 // Workgroup b takes columns
 // C (b % nblk) .. and part b / nblk of `parts`; the waves of all parts take
@@ -468,8 +475,8 @@ few_down_kernel(FewArgs a, int parts)
     __shared__ int last;
     const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    unsigned char *ring = smem + wave * kDownRing(XM);
-    float *ys = (float *)(smem + waves * kDownRing(XM));    // [waves][T][C]
+    unsigned char *ring = smem + wave * kDownRing(TERMS, XM);
+    float *ys = (float *)(smem + waves * kDownRing(TERMS, XM));    // [waves][T][C]
     float *y = ys + wave * a.T * C;
     for (int i = lane; i < a.T * C; i += 64) y[i] = 0.f;
     const int nblk = (a.d + C - 1) / C, part = blockIdx.x / nblk, blk = blockIdx.x - part * nblk;
@@ -482,7 +489,7 @@ few_down_kernel(FewArgs a, int parts)
         for (int s = beg; s < end;) {
             const int i = s / blocks, b0 = s - i * blocks, b1 = min(blocks, b0 + end - s);
             s += b1 - b0;
-            down_wave<BF16, TERMS, NM, XM, kDownDepth(XM, XM)>(a, ring, y, a.tab.rec[i], 0, 1, n0, b0, b1, blocks, lane);
+            down_wave<BF16, TERMS, NM, XM, kDownDepth(TERMS, XM, XM)>(a, ring, y, a.tab.rec[i], 0, 1, n0, b0, b1, blocks, lane);
         }
     } else {
         // a list entry's w is the cost of the blocks of one column before it / blocks
@@ -506,7 +513,7 @@ few_down_kernel(FewArgs a, int parts)
                 const int rows = down_rows(m, TERMS);
                 auto pass = [&](auto xr) {
                     constexpr int XR = decltype(xr)::value;
-                    down_wave<BF16, TERMS, NM, XR, kDownDepth(XM, XR)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
+                    down_wave<BF16, TERMS, NM, XR, kDownDepth(TERMS, XM, XR)>(a, ring, y, rec, first, m, n0, b0, b1, blocks, lane);
                 };
                 if (XM == 8 || rows == 8) pass(std::integral_constant<int, 8>());
                 else if (XM == 16 || rows == 16) pass(std::integral_constant<int, XM < 16 ? XM : 16>());
@@ -598,7 +605,7 @@ hipError_t down(const FewArgs &a, hipStream_t s)
 {
     constexpr int W = 4;
     constexpr int C = 16 * kDownM(XM);
-    const size_t lds = (size_t)W * (kDownRing(XM) + a.T * C * 4);
+    const size_t lds = (size_t)W * (kDownRing(TERMS, XM) + a.T * C * 4);
     const hipError_t e = allow_lds((const void *)few_down_kernel<BF16, TERMS, XM>, lds);
     if (e != hipSuccess) return e;
     const int parts = few_parts(a.T, a.d, a.f, a.E, a.k, a.S);
@@ -617,6 +624,7 @@ hipError_t down_for(const FewArgs &a, hipStream_t s)
             return a.T <= 8 ? down<BF16, 2, 16>(a, s) : down<BF16, 2, 32>(a, s);
         }
     if (a.T == 1) return down<BF16, 3, 4>(a, s);
+    if (a.T <= 2) return down<BF16, 3, 8>(a, s);
     if (a.T <= 5) return down<BF16, 3, 16>(a, s);
     return a.T <= 8 ? down<BF16, 3, 24>(a, s) : down<BF16, 3, 48>(a, s);
 }
@@ -651,8 +659,9 @@ int few_parts(int T, int d, int f, int E, int k, int S)
     return p;
 }
 
-// (measured, us, two terms and three: 32 tokens of 64 experts of 2048 x 1408, top-6, 197 and
-// 204, of which y twice as wide is a part; 4 tokens of 8 of 4096 x 14336 327 and 333)
+// (the layer in us, two terms and an fp16 y, three and an fp32 y: 64 experts of 2048 x
+// 1408, top-6, 4 tokens 82 and 83, 32 224 and 231; 8 of 4096 x 14336, top-2, 312 and 315,
+// 491 and 511)
 static int few_terms(int bf16, int ydt) { return !bf16 && ydt == 0 ? 2 : kFewTerms; }
 
 hipError_t launch_few(const FewArgs &args, hipStream_t s)
