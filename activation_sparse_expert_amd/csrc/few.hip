@@ -455,7 +455,8 @@ __device__ __forceinline__ void down_wave(const FewArgs &a, unsigned char *ring,
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float v = y[at[j] + 16 * m + i];
-                        if (h == 0 || fabsf(v) < INFINITY) y[at[j] + 16 * m + i] = v + w[j] * acc[m][j][i];
+                        const float c = w[j] * acc[m][j][i];
+                        y[at[j] + 16 * m + i] = v + (h == 0 || fabsf(v) < INFINITY ? c : 0.f);
                     }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
