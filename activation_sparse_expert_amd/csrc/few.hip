@@ -12,8 +12,8 @@
 // Before them the router, unless it is so small that every gate/up workgroup
 // works it out for itself (see launch_few).
 // 64 experts of 2048 x 1408, top-6, and 2 shared ones: one token 32 us (139 MB in
-// kernels of 3.1 + 18.3 + 12.1 us, short streams), 32 tokens 220 us (1.1 GB, 5.0
-// TB/s: 4.6 + 10.4 + 125 + 86).  8 of 4096 x 14336, top-2, 4 tokens (5 or 6 of them
+// kernels of 3.1 + 18.3 + 12.5 us, short streams), 32 tokens 200-209 us (1.1 GB, 5.3
+// TB/s: 4.5 + 10.6 + 125 + 68).  8 of 4096 x 14336, top-2, 4 tokens (5 or 6 of them
 // chosen): 297-351 us, gate/up at 6.1-6.3 TB/s.
 // h is kept as a sum of terms of the 16-bit type, each the rounding of what those
 // before it leave: three, which hold the 24 bits of fp32 (two bf16 terms would hold 17,
