@@ -16,11 +16,12 @@
 // TB/s: 4.5 + 10.6 + 125 + 68).  8 of 4096 x 14336, top-2, 4 tokens (5 or 6 of them
 // chosen): 297-351 us, gate/up at 6.1-6.3 TB/s.
 // h is kept as a sum of terms of the 16-bit type, each the rounding of what those
-// before it leave: three, which hold the 24 bits of fp32 (two bf16 terms would hold 17,
-// and turn one rounding of a bf16 y in a thousand), or two where both the type and y are
-// fp16: 22 bits, of which y shows 11.  In fp16 the second is kept times 2^11 and the third times
-// 2^22 (kTermScale), since the rest of an h below 2^-3 lies among fp16's subnormals,
-// whose steps are coarser than 2^-22 of it; of h down to 2^-14 lo then loses nothing.
+// before it leave: three, which hold the 24 bits of fp32 (two of bf16 hold 17, which
+// turns one rounding of a bf16 y in a thousand), or two where the layer and y are both
+// fp16: 22 bits, of which y shows 11.  In fp16 the second is kept times 2^11 and the
+// third times 2^22 (kTermScale), since the rest of an h below 2^-3 lies among fp16's
+// subnormals, whose steps are coarser than 2^-22 of it; of an h down to 2^-14 the
+// second then loses nothing.
 // The terms go through the matrix core as tokens of their own, which mostly fill
 // columns that would idle.  A column of the matrix core depends on its own token
 // alone, so infinities and NaN stay with the tokens whose experts hold them.

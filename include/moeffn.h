@@ -349,8 +349,8 @@ moe_status moe_layer_forward(const moe_layer *L, const void *x, moe_dtype xdt, i
  *   NULL; residual and x may be y itself.  SiLU(g) u is kept to fp32's 24 bits
  *   (fp16 layers: to 2^-47 where it is below 2^-24), in fp16 layers whose y is fp16 to 22
  *   (to 2^-36 where it is below 2^-14); in fp16 layers it is infinite beyond 65504.
- *   All sums are fp32.  Bit-reproducible for the same call; the order of a token's sums may depend
- *   on which experts the call's other tokens chose.
+ *   All sums are fp32.  Bit-reproducible for the same call; the order of a token's
+ *   sums may depend on which experts the call's other tokens chose.
  * trace as moe_layer_forward's for the dense path (no masks, bits or nnz).
  * Limits: T <= 32, d <= 16384, T (k + S) <= 2048 (else MOE_ERR_UNSUPPORTED); E <= 1024,
  * k <= E (else MOE_ERR_INVALID_ARG).

@@ -1,8 +1,6 @@
 """The linear layer's tile kernels against 64 bits: every tile, plain and gated,
 with and without a split of k; strides, special values, streams and graphs in
 them (sizes that tests/test_linear_gpu.py streams past the tokens instead)."""
-import threading
-
 import pytest
 import torch
 
