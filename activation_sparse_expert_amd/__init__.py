@@ -16,11 +16,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # MOEFFN_LIB names another build of the same sources (the sanitizer build)
 LIB_PATH = os.environ.get("MOEFFN_LIB") or os.path.join(HERE, "libmoeffn.so")
 
-MOE_F16, MOE_BF16, MOE_F32 = 0, 1, 2
+MOE_F16, MOE_BF16, MOE_F32, MOE_I8 = 0, 1, 2, 3
 PATH_SPARSE, PATH_DENSE, PATH_AUTO, PATH_MIXED = 0, 1, 2, 3
 OP_EXPERT, OP_ROUTE, OP_LAYER, OP_CALIBRATE, OP_EAMC, OP_EXPERT_BITS = 0, 1, 2, 3, 4, 5
-OP_LINEAR, OP_LAYER_FEW = 6, 7
+OP_LINEAR, OP_LAYER_FEW, OP_LINEAR_Q8 = 6, 7, 8
 ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+NORM = {"rms": 0, "layer": 1}
 
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
           -3: "MOE_ERR_ALIGNMENT", -4: "MOE_ERR_WORKSPACE", -5: "MOE_ERR_HIP"}
@@ -32,7 +33,8 @@ EXPORTED = ["moe_route_topk", "moe_expert_forward_sparse", "moe_layer_forward",
             "moe_build_sources_sha256", "moe_expert_forward_sparse_noalloc",
             "moe_noalloc_scratch_bytes", "moe_materialize_up", "moe_transpose_down",
             "moe_auto_dense_min", "moe_mixed_dense_min", "moe_layer_forward_few",
-            "moe_linear_forward", "moe_linear_plan"]
+            "moe_linear_forward", "moe_linear_plan", "moe_linear_q8_forward", "moe_quantize_rows",
+            "moe_dequantize_rows", "moe_norm_forward"]
 
 
 class MoeError(RuntimeError):
@@ -65,6 +67,17 @@ class LinearDesc(C.Structure):
     _fields_ = [("n", C.c_int), ("k", C.c_int), ("wdt", C.c_int), ("w", C.c_void_p),
                 ("bias", C.c_void_p), ("w_gate", C.c_void_p), ("bias_gate", C.c_void_p),
                 ("act", C.c_int)]
+
+
+class LinearQ8Desc(C.Structure):
+    _fields_ = [("n", C.c_int), ("k", C.c_int), ("w", C.c_void_p), ("w_scale", C.c_void_p), ("bias", C.c_void_p),
+                ("w_gate", C.c_void_p), ("gate_scale", C.c_void_p), ("bias_gate", C.c_void_p), ("act", C.c_int)]
+
+
+class NormDesc(C.Structure):
+    _fields_ = [("d", C.c_int), ("kind", C.c_int), ("eps", C.c_float), ("wdt", C.c_int), ("w", C.c_void_p),
+                ("b", C.c_void_p), ("post", C.c_int), ("post_w", C.c_void_p), ("post_b", C.c_void_p),
+                ("offset", C.c_int), ("residual_scale", C.c_float), ("block_scale", C.c_float)]
 
 
 _lib = None
@@ -133,6 +146,15 @@ def lib():
         L.moe_linear_forward.restype = I
         L.moe_linear_forward.argtypes = [C.POINTER(LinearDesc), P, I, C.c_longlong, I, P,
                                          C.c_longlong, P, I, C.c_longlong, P, Z, P]
+        N = C.c_longlong
+        L.moe_linear_q8_forward.restype = I
+        L.moe_linear_q8_forward.argtypes = [C.POINTER(LinearQ8Desc), P, I, N, P, I, P, N, P, I, N, P, Z, P]
+        L.moe_quantize_rows.restype = I
+        L.moe_quantize_rows.argtypes = [P, I, N, I, I, P, N, P, P]
+        L.moe_dequantize_rows.restype = I
+        L.moe_dequantize_rows.argtypes = [P, N, P, I, I, P, I, N, P]
+        L.moe_norm_forward.restype = I
+        L.moe_norm_forward.argtypes = [C.POINTER(NormDesc), I, P, I, N, P, I, N, P, N, P, N, P, I, N, P, P]
         L.moe_linear_plan.restype = I
         L.moe_linear_plan.argtypes = [I, I, I, I, C.POINTER(I), C.POINTER(I)]
         _lib = L
@@ -531,6 +553,213 @@ def linear_plan(T: int, k: int, n: int, gated: bool = False):
     if parts < 0:
         raise ValueError(f"the linear layer does not take T = {T}, k = {k}, n = {n}")
     return ((tokens.value, rows.value) if parts else None), parts
+
+
+@dataclass
+class LinearQ8:
+    """A linear layer on 8-bit weights: output j's weights are w_scale[j] w[j] (quantize_rows
+    makes both from [n][k] weights), plain or gated as Linear."""
+    w: "torch.Tensor"                            # [n][k] int8
+    w_scale: "torch.Tensor"                      # [n] fp32
+    bias: Optional["torch.Tensor"] = None        # [n] fp32
+    w_gate: Optional["torch.Tensor"] = None      # [n][k] int8
+    gate_scale: Optional["torch.Tensor"] = None  # [n] fp32
+    bias_gate: Optional["torch.Tensor"] = None   # [n] fp32
+    act: str = "none"                            # a key of ACT
+
+    @property
+    def n(self):
+        return self.w.shape[0]
+
+    @property
+    def k(self):
+        return self.w.shape[1]
+
+    def desc(self) -> LinearQ8Desc:
+        if self.act not in ACT:
+            raise ValueError(f"act must be one of {sorted(ACT)}")
+        return LinearQ8Desc(self.w.shape[0], self.w.shape[1], _ptr(self.w), _ptr(self.w_scale), _ptr(self.bias),
+                            _ptr(self.w_gate), _ptr(self.gate_scale), _ptr(self.bias_gate), ACT[self.act])
+
+
+def _row_dt(t) -> int:
+    import torch
+    return MOE_I8 if t.dtype == torch.int8 else _dt(t)
+
+
+def linear_q8_forward(linear: LinearQ8, x, *, x_scale=None, residual=None, y=None, out_dtype=None, ws=None):
+    """residual + the linear layer on x [T][k]: int8 codes with x_scale [T] (quantize_rows,
+    norm_forward), or fp16, bf16 or fp32, which the call makes codes of; returns y [T][n].
+
+    x, y and residual may be row-strided (contiguous rows; x's row stride a
+    multiple of 16).  ``residual`` has y's type and may be y."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [T][k]")
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    w = linear.w
+    T, (n, k) = x.shape[0], w.shape
+    _want("x", x, device, (T, k))
+    xdt = _row_dt(x)
+    if (x_scale is None) == (xdt == MOE_I8):
+        raise ValueError("x_scale comes with int8 codes and with nothing else")
+    _want("x_scale", x_scale, device, (T,), torch.float32)
+    _want("w", w, device, (n, k), torch.int8)
+    _want("w_scale", linear.w_scale, device, (n,), torch.float32)
+    _want("bias", linear.bias, device, (n,), torch.float32)
+    if (linear.w_gate is None) != (linear.gate_scale is None):
+        raise ValueError("w_gate and gate_scale come together")
+    _want("w_gate", linear.w_gate, device, (n, k), torch.int8)
+    _want("gate_scale", linear.gate_scale, device, (n,), torch.float32)
+    _want("bias_gate", linear.bias_gate, device, (n,), torch.float32)
+    if y is None:
+        y = torch.empty((T, n), dtype=out_dtype or torch.float32, device=device)
+    else:
+        _want("y", y, device, (T, n))
+    _want("residual", residual, device, (T, n), y.dtype)
+    xp, xs = _rows("x", x, 16)
+    yp, ys = _rows("y", y)
+    rp, rs = _rows("residual", residual) if residual is not None else (None, 0)
+    ws, wp, wb = _workspace(torch, device, _size_of(OP_LINEAR_Q8, T, k, n, xdt, 0, 0), ws)
+    _call(torch, device, "moe_linear_q8_forward", lib().moe_linear_q8_forward, C.byref(linear.desc()), xp, xdt,
+          xs, _ptr(x_scale), T, rp, rs, yp, _dt(y), ys, wp, wb)
+    return y
+
+
+def quantize_rows(x, *, q=None, scale=None):
+    """Rows of x [T][k] (fp16, bf16, fp32) as int8 codes q = round(127 x / max|x|), ties to
+    even, with the scale max|x| / 127 of each row; returns (q [T][k], scale [T] fp32).
+    Tokens for linear_q8_forward, or the weights [n][k] of a LinearQ8."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [T][k]")
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    T, k = x.shape
+    if q is None:
+        q = torch.empty((T, k), dtype=torch.int8, device=device)
+    else:
+        _want("q", q, device, (T, k), torch.int8)
+    if scale is None:
+        scale = torch.empty(T, dtype=torch.float32, device=device)
+    else:
+        _want("scale", scale, device, (T,), torch.float32)
+    xp, xs = _rows("x", x)
+    qp, qs = _rows("q", q)
+    _call(torch, device, "moe_quantize_rows", lib().moe_quantize_rows, xp, _dt(x), xs, T, k, qp, qs, _ptr(scale))
+    return q, scale
+
+
+def dequantize_rows(q, scale, *, y=None, out_dtype=None):
+    """The values q scale [T][k] that int8 codes [T][k] and their scales [T] stand for."""
+    import torch
+    if q.dim() != 2:
+        raise ValueError("q must be [T][k]")
+    device = q.device
+    if device.type != "cuda":
+        raise ValueError("q must be a GPU tensor")
+    T, k = q.shape
+    _want("q", q, device, (T, k), torch.int8)
+    _want("scale", scale, device, (T,), torch.float32)
+    if y is None:
+        y = torch.empty((T, k), dtype=out_dtype or torch.float32, device=device)
+    else:
+        _want("y", y, device, (T, k))
+    qp, qs = _rows("q", q)
+    yp, ys = _rows("y", y)
+    _call(torch, device, "moe_dequantize_rows", lib().moe_dequantize_rows, qp, qs, _ptr(scale), T, k, yp, _dt(y), ys)
+    return y
+
+
+@dataclass
+class Norm:
+    """The norms between two blocks (norm_forward): RMS or layer norms of d channels."""
+    d: int
+    kind: str = "rms"                           # a key of NORM, for both norms
+    eps: float = 1e-6
+    w: Optional["torch.Tensor"] = None          # [d] of the norm before the next block (None: 1)
+    b: Optional["torch.Tensor"] = None          # [d] (None: 0)
+    post: bool = False                          # whether the block's output is normed too
+    post_w: Optional["torch.Tensor"] = None     # [d]
+    post_b: Optional["torch.Tensor"] = None     # [d]
+    offset: bool = False                        # the weights are 1 + w, 1 + post_w
+    residual_scale: float = 1.0
+    block_scale: float = 1.0
+
+    def desc(self) -> NormDesc:
+        if self.kind not in NORM:
+            raise ValueError(f"kind must be one of {sorted(NORM)}")
+        given = [t for t in (self.w, self.b, self.post_w, self.post_b) if t is not None]
+        if any(t.dtype != given[0].dtype for t in given):
+            raise TypeError("the norms' weights and biases must have one dtype")
+        return NormDesc(self.d, NORM[self.kind], self.eps, _dt(given[0]) if given else MOE_F32, _ptr(self.w),
+                        _ptr(self.b), int(bool(self.post)), _ptr(self.post_w), _ptr(self.post_b),
+                        int(bool(self.offset)), self.residual_scale, self.block_scale)
+
+
+def norm_forward(norm: Norm, residual, block=None, *, gate=None, y=None, out=None, out_dtype=None, out_scale=None):
+    """Between two blocks: the first one's output, normed or not, gated and scaled, is added to
+    the residual stream, and the norm before the second one is taken:
+    v = residual_scale residual + block_scale (gate * Npost(block)), y = v, out = N(v).
+
+    residual [T][d] or None (0); block [T][d] or None; gate, of the block's type, [T][d] or
+    [d].  Returns (y, out, out_scale): y has the residual's type (without a residual the
+    block's) and may be the residual, without a block it is written only if given; out has
+    out_dtype, by default the block's or the residual's type, or as torch.int8 the codes of
+    N(v) with out_scale [T].  y or out False: not wanted (None is returned)."""
+    import torch
+    x = residual if residual is not None else block
+    if x is None:
+        raise ValueError("norm_forward needs a residual or a block")
+    if x.dim() != 2:
+        raise ValueError("residual and block must be [T][d]")
+    device = x.device
+    if device.type != "cuda":
+        raise ValueError("residual and block must be GPU tensors")
+    T, d = x.shape
+    shape = (T, d)
+    if d != norm.d:
+        raise ValueError(f"the rows have {d} columns, the norm d = {norm.d}")
+    for name in ("w", "b", "post_w", "post_b"):
+        t = getattr(norm, name)
+        if t is not None:
+            _want(name, t, device, (d,))
+    rp, rs, bp, bs, gp, gs = None, 0, None, 0, None, 0
+    if residual is not None:
+        rp, rs = _rows("residual", residual)
+    if block is not None:
+        _want("block", block, device, shape)
+        bp, bs = _rows("block", block)
+    if gate is not None:
+        if block is None:
+            raise ValueError("a gate needs a block")
+        if gate.dim() == 1:
+            _want("gate", gate, device, (d,), block.dtype)
+            gp = _ptr(gate)
+        else:
+            _want("gate", gate, device, shape, block.dtype)
+            gp, gs = _rows("gate", gate)
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype, device=device) if block is not None else False
+    elif y is not False:
+        _want("y", y, device, shape, x.dtype)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or (block if block is not None else x).dtype, device=device)
+    elif out is not False:
+        _want("out", out, device, shape)
+    yp, ys = _rows("y", y) if y is not False else (None, 0)
+    op, os_ = _rows("out", out) if out is not False else (None, 0)
+    codes = out is not False and out.dtype == torch.int8
+    if codes and out_scale is None:
+        out_scale = torch.empty(T, dtype=torch.float32, device=device)
+    _want("out_scale", out_scale, device, (T,), torch.float32)
+    _call(torch, device, "moe_norm_forward", lib().moe_norm_forward, C.byref(norm.desc()), T, rp, _dt(x), rs, bp,
+          _dt(block) if block is not None else 0, bs, gp, gs, yp, ys, op, _row_dt(out) if op is not None else 0, os_,
+          _ptr(out_scale))
+    return y if y is not False else None, out if out is not False else None, out_scale
 
 
 def calibrate_threshold(v, q: float, *, out=None, ws=None):

@@ -13,7 +13,8 @@ BUILD = os.path.join(HERE, "_build")
 
 SOURCES = ["api.cpp", "expert_sparse_f16.hip", "expert_sparse_bf16.hip", "reduce.hip", "route.hip",
            "pack.hip", "dense_mfma.hip", "dense_gemm.hip", "calibrate.hip",
-           "eamc.hip", "expert_sparse_bits.hip", "linear_stream.hip", "linear_tile.hip", "few.hip"]
+           "eamc.hip", "expert_sparse_bits.hip", "linear_stream.hip", "linear_tile.hip", "few.hip",
+           "quantize.hip", "norm.hip", "linear_q8.hip"]
 
 HEADER = os.path.join(os.path.dirname(HERE), "include", "moeffn.h")
 

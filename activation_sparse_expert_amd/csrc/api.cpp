@@ -3,6 +3,7 @@
 // for an invalid request, so the error paths can be exercised without a GPU.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 #include <new>
@@ -10,6 +11,7 @@
 #include "../../include/moeffn.h"
 #include "internal.hpp"
 #include "linear.hpp"
+#include "rows.hpp"
 
 using namespace moeffn;
 
@@ -424,10 +426,35 @@ bool auto_dense(const moe_layer *L, int T)
 }
 
 constexpr int kLinearMaxT = 65536, kLinearMaxK = 1 << 20, kLinearMaxN = 1 << 24;
+constexpr int kLinearQ8MaxK = (1 << 17) - 16;       // sums of products of codes, 2^14 each at most, fit 32 bits
+constexpr int kRowsMaxK = 1 << 20, kNormMaxD = 16384;
 
 bool linear_size_ok(int T, int k, int n)
 {
     return T >= 1 && T <= kLinearMaxT && k >= 8 && k % 8 == 0 && k <= kLinearMaxK && n >= 1 && n <= kLinearMaxN;
+}
+
+// Codes of the tokens, their scales, and partial products
+struct LinearQ8Ws {
+    int8_t *q;
+    float *scale;
+    int32_t *part;
+};
+
+bool linear_q8_size_ok(int T, int k, int n)
+{
+    return T >= 1 && T <= kLinearMaxT && k >= 16 && k % 16 == 0 && k <= kLinearQ8MaxK && n >= 1 && n <= kLinearMaxN;
+}
+
+size_t linear_q8_ws_bytes(int T, int k, int n, bool codes, LinearQ8Ws *out, void *base)
+{
+    const size_t q = codes ? 0 : up((size_t)T * k), sc = codes ? 0 : up((size_t)T * 4);
+    if (out) {
+        out->q = (int8_t *)base;
+        out->scale = (float *)((char *)base + q);
+        out->part = (int32_t *)((char *)base + q + sc);
+    }
+    return q + sc + up(linear_q8_split_bytes(T, k, n));
 }
 
 bool few_size_ok(int T, int d, int f, int E, int k, int S)
@@ -518,6 +545,9 @@ size_t moe_workspace_size(moe_op op, int T, int d, int f, int E, int k, int S)
         return d > kEamcMaxLen ? 0 : up((size_t)T * 8);   // T stored EAMs of d entries
     case MOE_OP_LINEAR:
         return linear_size_ok(T, d, f) ? up(linear_ws_bytes(T, d, f)) : 0;
+    case MOE_OP_LINEAR_Q8:                              // E is the type of the tokens
+        if (!linear_q8_size_ok(T, d, f) || (E != MOE_I8 && !valid_out((moe_dtype)E))) return 0;
+        return linear_q8_ws_bytes(T, d, f, E == MOE_I8, nullptr, nullptr);
     case MOE_OP_LAYER_FEW:
         return few_size_ok(T, d, f, E, k, S) ? few_ws_bytes(T, d, f, E, k, S, nullptr, nullptr) : 0;
     }
@@ -1031,6 +1061,118 @@ int moe_linear_plan(int T, int k, int n, int gated, int *tokens, int *rows)
     if (tokens) *tokens = bm;
     if (rows) *rows = bn;
     return parts;
+}
+
+moe_status moe_linear_q8_forward(const moe_linear_q8 *L, const void *x, moe_dtype xdt, long long x_stride,
+                                 const float *x_scale, int T, const void *residual,
+                                 long long residual_stride, void *y, moe_dtype ydt, long long y_stride,
+                                 void *ws, size_t ws_bytes, void *stream)
+{
+    if (!L || !x || !y || !L->w || !L->w_scale) return MOE_ERR_INVALID_ARG;
+    const int n = L->n, k = L->k;
+    if (T < 1 || T > kLinearMaxT || n < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+    if (L->act < MOE_ACT_NONE || L->act > MOE_ACT_SILU) return MOE_ERR_INVALID_ARG;
+    if (L->w_gate ? !L->gate_scale : L->gate_scale || L->bias_gate) return MOE_ERR_INVALID_ARG;
+    if (x_stride < k || y_stride < n || (residual && residual_stride < n)) return MOE_ERR_INVALID_ARG;
+    if (residual == y && residual_stride != y_stride) return MOE_ERR_INVALID_ARG;
+    if (!linear_q8_size_ok(T, k, n)) return MOE_ERR_UNSUPPORTED;
+    if ((xdt != MOE_I8 && !valid_out(xdt)) || !valid_out(ydt)) return MOE_ERR_UNSUPPORTED;
+    const bool given = xdt == MOE_I8;                   // the tokens come as codes
+    if (given ? !x_scale : x_scale != nullptr) return MOE_ERR_INVALID_ARG;
+    const size_t ya = ydt == MOE_F32 ? 4 : 2;
+    if (!aligned(x, 16) || x_stride % 16 != 0 || !aligned(L->w, 16) || !aligned(L->w_gate, 16) || !aligned(y, ya) ||
+        !aligned(residual, ya) || !aligned(L->w_scale, 4) || !aligned(L->gate_scale, 4) || !aligned(L->bias, 4) ||
+        !aligned(L->bias_gate, 4) || !aligned(x_scale, 4))
+        return MOE_ERR_ALIGNMENT;
+    const size_t need = linear_q8_ws_bytes(T, k, n, given, nullptr, nullptr);
+    if (need && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+    if (!aligned(ws, 16)) return MOE_ERR_ALIGNMENT;
+    if (x == y) return MOE_ERR_INVALID_ARG;             // other workgroups may not have read it
+    LinearQ8Ws w;
+    linear_q8_ws_bytes(T, k, n, given, &w, ws);
+    hipStream_t s = (hipStream_t)stream;
+    LinearQ8Args a{};
+    a.T = T; a.K = k; a.N = n;
+    a.act = (int)L->act; a.ydt = (int)ydt;
+    a.x = (const uint16_t *)x; a.xs = x_stride; a.sx = x_scale;
+    a.w = (const uint16_t *)L->w; a.wg = (const uint16_t *)L->w_gate;
+    a.sw = L->w_scale; a.sg = L->gate_scale;
+    a.b = L->bias; a.bg = L->bias_gate;
+    a.r = residual; a.rs = residual_stride;
+    a.y = y; a.ys = y_stride;
+    a.part = (float *)w.part;
+    if (!given) {
+        QuantizeArgs q{T, k, x, (int)xdt, x_stride, w.q, k, w.scale};
+        const hipError_t e = launch_quantize_rows(q, s);
+        if (e != hipSuccess) return MOE_ERR_HIP;
+        a.x = (const uint16_t *)w.q; a.xs = k; a.sx = w.scale;
+    }
+    return hip_status(launch_linear_q8(a, s));
+}
+
+moe_status moe_quantize_rows(const void *x, moe_dtype xdt, long long x_stride, int T, int k, int8_t *q,
+                             long long q_stride, float *scale, void *stream)
+{
+    if (!x || !q || !scale || T < 1 || k < 1 || x_stride < k || q_stride < k) return MOE_ERR_INVALID_ARG;
+    if (x == (const void *)q || x == (const void *)scale || (const void *)q == (const void *)scale)
+        return MOE_ERR_INVALID_ARG;
+    if (k > kRowsMaxK || !valid_out(xdt)) return MOE_ERR_UNSUPPORTED;
+    if (!aligned(x, xdt == MOE_F32 ? 4 : 2) || !aligned(scale, 4)) return MOE_ERR_ALIGNMENT;
+    const QuantizeArgs a{T, k, x, (int)xdt, x_stride, q, q_stride, scale};
+    return hip_status(launch_quantize_rows(a, (hipStream_t)stream));
+}
+
+moe_status moe_dequantize_rows(const int8_t *q, long long q_stride, const float *scale, int T, int k, void *y,
+                               moe_dtype ydt, long long y_stride, void *stream)
+{
+    if (!q || !scale || !y || T < 1 || k < 1 || q_stride < k || y_stride < k) return MOE_ERR_INVALID_ARG;
+    if ((const void *)q == y || (const void *)scale == y) return MOE_ERR_INVALID_ARG;
+    if (k > kRowsMaxK || !valid_out(ydt)) return MOE_ERR_UNSUPPORTED;
+    if (!aligned(y, ydt == MOE_F32 ? 4 : 2) || !aligned(scale, 4)) return MOE_ERR_ALIGNMENT;
+    const DequantizeArgs a{T, k, q, q_stride, scale, y, (int)ydt, y_stride};
+    return hip_status(launch_dequantize_rows(a, (hipStream_t)stream));
+}
+
+moe_status moe_norm_forward(const moe_norm *N, int T, const void *residual, moe_dtype rdt,
+                            long long residual_stride, const void *block, moe_dtype bdt,
+                            long long block_stride, const void *gate, long long gate_stride, void *y,
+                            long long y_stride, void *out, moe_dtype odt, long long out_stride,
+                            float *out_scale, void *stream)
+{
+    if (!N || T < 1 || (!residual && !block) || (!y && !out)) return MOE_ERR_INVALID_ARG;
+    const int d = N->d;
+    if (d < 1 || (N->kind != MOE_NORM_RMS && N->kind != MOE_NORM_LAYER)) return MOE_ERR_INVALID_ARG;
+    if (!(N->eps >= FLT_MIN && N->eps <= FLT_MAX)) return MOE_ERR_INVALID_ARG;
+    if ((!N->post && (N->post_w || N->post_b)) || (!block && (N->post || gate))) return MOE_ERR_INVALID_ARG;
+    if ((residual && residual_stride < d) || (block && block_stride < d) || (y && y_stride < d) ||
+        (out && out_stride < d) || (gate && gate_stride != 0 && gate_stride < d))
+        return MOE_ERR_INVALID_ARG;
+    if (y && (y == block || y == gate || (y == residual && y_stride != residual_stride))) return MOE_ERR_INVALID_ARG;
+    if (out && (out == y || out == residual || out == block || out == gate)) return MOE_ERR_INVALID_ARG;
+    if (d > kNormMaxD) return MOE_ERR_UNSUPPORTED;
+    const bool codes = out && odt == MOE_I8, weights = N->w || N->b || N->post_w || N->post_b;
+    if (((residual || y) && !valid_out(rdt)) || (block && !valid_out(bdt)) || (out && !codes && !valid_out(odt)) ||
+        (weights && !valid_out(N->wdt)))
+        return MOE_ERR_UNSUPPORTED;
+    if (codes != (out_scale != nullptr)) return MOE_ERR_INVALID_ARG;
+    auto fits = [](const void *p, moe_dtype t) { return aligned(p, (size_t)type_bytes((int)t)); };
+    if (!fits(residual, rdt) || !fits(y, rdt) || !fits(block, bdt) || !fits(gate, bdt) || !fits(out, odt) ||
+        !fits(N->w, N->wdt) || !fits(N->b, N->wdt) || !fits(N->post_w, N->wdt) || !fits(N->post_b, N->wdt) ||
+        !aligned(out_scale, 4))
+        return MOE_ERR_ALIGNMENT;
+    NormArgs a{};
+    a.T = T; a.d = d;
+    a.layer = N->kind == MOE_NORM_LAYER ? 1 : 0; a.eps = N->eps;
+    a.wdt = (int)N->wdt; a.w = N->w; a.b = N->b;
+    a.post = N->post ? 1 : 0; a.pw = N->post_w; a.pb = N->post_b;
+    a.add = N->offset ? 1.f : 0.f;
+    a.rscale = N->residual_scale; a.bscale = N->block_scale;
+    a.r = residual; a.rdt = (int)rdt; a.rs = residual_stride;
+    a.o = block; a.odt = (int)bdt; a.os = block_stride;
+    a.g = gate; a.gs = gate_stride;
+    a.y = y; a.ys = y_stride;
+    a.out = out; a.ndt = (int)odt; a.ns = out_stride; a.out_scale = out_scale;
+    return hip_status(launch_norm(a, (hipStream_t)stream));
 }
 
 moe_status moe_pack_up_int2(const void *w_up_t, moe_dtype dt, int d, int f, uint8_t *up_q,

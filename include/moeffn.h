@@ -90,7 +90,12 @@ typedef MOE_ENUM {
     MOE_ERR_HIP = -5            /* a HIP runtime call or kernel launch failed    */
 } moe_status;
 
-typedef MOE_ENUM { MOE_F16 = 0, MOE_BF16 = 1, MOE_F32 = 2 } moe_dtype;
+typedef MOE_ENUM {
+    MOE_F16 = 0,
+    MOE_BF16 = 1,
+    MOE_F32 = 2,
+    MOE_I8 = 3                  /* 8-bit codes with a scale for each row, where a call names it */
+} moe_dtype;
 
 typedef MOE_ENUM {
     MOE_PATH_SPARSE = 0,        /* Algorithm 1: INT2 up, threshold mask, row gathers */
@@ -107,7 +112,8 @@ typedef MOE_ENUM {
     MOE_OP_EAMC = 4,            /* moe_eamc_match (T = n, d = len) */
     MOE_OP_EXPERT_BITS = 5,     /* moe_expert_forward_sparse_bits, any width */
     MOE_OP_LINEAR = 6,          /* moe_linear_forward (d = inputs, f = outputs) */
-    MOE_OP_LAYER_FEW = 7        /* moe_layer_forward_few    */
+    MOE_OP_LAYER_FEW = 7,       /* moe_layer_forward_few    */
+    MOE_OP_LINEAR_Q8 = 8        /* moe_linear_q8_forward (d = inputs, f = outputs, E = type of x) */
 } moe_op;
 
 typedef MOE_ENUM {
@@ -117,6 +123,11 @@ typedef MOE_ENUM {
     MOE_ACT_GELU_TANH = 3,      /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
     MOE_ACT_SILU = 4            /* v / (1 + exp(-v)) */
 } moe_act;
+
+typedef MOE_ENUM {
+    MOE_NORM_RMS = 0,           /* v / sqrt(mean(v^2) + eps)               */
+    MOE_NORM_LAYER = 1          /* the same of v - mean(v)                 */
+} moe_norm_kind;
 
 /* One compressed expert (FloE review, "混合压缩策略": {W^S(gate), W^S(down),
  * W^Q(up)}; Algorithm 1 inputs E_ij and t_ij). */
@@ -170,6 +181,32 @@ typedef struct {
     const float *bias_gate;     /* [n] or NULL (gated layers only)         */
     moe_act act;                /* of the product, or of the gate's when gated */
 } moe_linear;
+
+/* One linear layer on 8-bit weights, plain or gated (moe_linear_q8_forward): the weight of
+ * output j and input i is w_scale[j] w[j][i] (moe_quantize_rows makes both). */
+typedef struct {
+    int n, k;                   /* outputs, inputs                         */
+    const int8_t *w;            /* [n][k] codes                            */
+    const float *w_scale;       /* [n]                                     */
+    const float *bias;          /* [n] or NULL                             */
+    const int8_t *w_gate;       /* [n][k] codes of W^gate; NULL: not gated */
+    const float *gate_scale;    /* [n] (gated layers only)                 */
+    const float *bias_gate;     /* [n] or NULL (gated layers only)         */
+    moe_act act;                /* of the product, or of the gate's when gated */
+} moe_linear_q8;
+
+/* The norms between two blocks (moe_norm_forward).  NULL weights are 1, NULL biases 0. */
+typedef struct {
+    int d;
+    moe_norm_kind kind;         /* of both norms                           */
+    float eps;                  /* from FLT_MIN                            */
+    moe_dtype wdt;              /* type of the weights and biases          */
+    const void *w, *b;          /* [d] of the norm before the next block   */
+    int post;                   /* 1: the block's output is normed too     */
+    const void *post_w, *post_b; /* [d] of that norm                       */
+    int offset;                 /* 1: the weights are 1 + w, 1 + post_w    */
+    float residual_scale, block_scale;
+} moe_norm;
 
 /* Optional device outputs of moe_layer_forward (any field may be NULL). */
 typedef struct {
@@ -392,6 +429,68 @@ moe_status moe_linear_forward(const moe_linear *L, const void *x, moe_dtype xdt,
  * Either pointer may be NULL.
  */
 int moe_linear_plan(int T, int k, int n, int gated, int *tokens, int *rows);
+
+/*
+ * The linear layer on 8-bit integers, weights and tokens alike, with a scale for each token
+ * and each output:
+ *   v_tj = sx_t sw_j sum_i xq_ti wq_ji,   y = residual + act(v + bias), or with L->w_gate
+ *   y = residual + act(vg + bias_gate) (.) (v + bias)
+ * The sums of products of codes are exact (32-bit integers); scales, bias and activation
+ * are applied in fp32 as moe_linear_forward's are, with one rounding to ydt.
+ *   x [T][k] in xdt: MOE_I8 codes (any from -128 to 127) with x_scale [T], or MOE_F16,
+ *   MOE_BF16 or MOE_F32 (x_scale NULL), which the call makes codes of by
+ *   moe_quantize_rows' rule.  A token whose scale is NaN has a row of NaN.
+ *   y [T][n] in ydt, residual [T][n] in ydt or NULL; rows at x_stride (a multiple of 16),
+ *   y_stride and residual_stride elements.  residual may be y itself, at the same stride;
+ *   y must not overlap x (x == y: MOE_ERR_INVALID_ARG) or the weights otherwise.
+ * Limits: 1 <= T <= 65536 (else MOE_ERR_INVALID_ARG); k a multiple of 16 up to 2^17 - 16, n
+ * up to 2^24 (else MOE_ERR_UNSUPPORTED); x and the weights 16-byte aligned.  Outputs are
+ * bit-reproducible.
+ * Workspace: moe_workspace_size(MOE_OP_LINEAR_Q8, T, k, n, xdt, 0, 0) bytes, gated or not;
+ * where that is 0 ws may be NULL.
+ */
+moe_status moe_linear_q8_forward(const moe_linear_q8 *L, const void *x, moe_dtype xdt, long long x_stride,
+                                 const float *x_scale, int T, const void *residual,
+                                 long long residual_stride, void *y, moe_dtype ydt, long long y_stride,
+                                 void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Rows to 8-bit codes: q_ti = round(127 x_ti / a_t), ties to even, scale_t = a_t / 127 in fp32,
+ * a_t = max_i |x_ti|; a weight [n][k] has a scale for each output this way, tokens [T][k] one for
+ * each token.  The codes are those of exact arithmetic.  A row of zeros has the scale
+ * 0; a row with an infinity or NaN has the scale NaN and codes 0, so that what is
+ * made of it is NaN.  (Below a_t = 2^-119 the scale is subnormal and keeps fewer bits.)
+ *   x [T][k] in xdt (f16, bf16, f32), rows at x_stride; q [T][k], rows at q_stride
+ *   (elements); scale [T].  q must not overlap x.  T >= 1, 1 <= k <= 2^20.
+ */
+moe_status moe_quantize_rows(const void *x, moe_dtype xdt, long long x_stride, int T, int k, int8_t *q,
+                             long long q_stride, float *scale, void *stream);
+
+/* The values that codes stand for: y_ti = q_ti scale_t in fp32, rounded to ydt (f16, bf16, f32);
+ * infinite where that passes the type, as 127 scale_t does where a_t was fp32's largest value.
+ * Limits as moe_quantize_rows'; y must not overlap q. */
+moe_status moe_dequantize_rows(const int8_t *q, long long q_stride, const float *scale, int T, int k, void *y,
+                               moe_dtype ydt, long long y_stride, void *stream);
+
+/*
+ * Between two blocks of a model: the first one's output, normed or not, gated and scaled, is
+ * added to the residual stream, and the norm before the second one is taken:
+ *   v = residual_scale residual + block_scale (gate (.) Npost(block)),  y = v,  out = N(v),
+ *   N(v) = (v - m) / sqrt(mean((v - m)^2) + eps) (.) w + b,  m = mean(v) (RMS: 0).
+ * Everything is fp32 up to one rounding of each output; N is taken of the unrounded v.
+ *   residual [T][d] in rdt or NULL (0); block [T][d] in bdt or NULL (then no gate and no
+ *   post norm); gate in bdt: [T][d], one row of d for all tokens (gate_stride 0), or
+ *   NULL (1); y [T][d] in rdt or NULL (not wanted); out [T][d] in odt or NULL (not wanted).
+ *   odt MOE_I8: the codes of N(v) by moe_quantize_rows' rule, with out_scale [T] (NULL
+ *   for the other types).  Rows at the given strides, in elements.  y may be the residual,
+ *   at the same stride; outputs must not overlap inputs or each other otherwise.
+ * Limits: T >= 1, 1 <= d <= 16384 (else MOE_ERR_UNSUPPORTED).  Bit-reproducible.
+ */
+moe_status moe_norm_forward(const moe_norm *N, int T, const void *residual, moe_dtype rdt,
+                            long long residual_stride, const void *block, moe_dtype bdt,
+                            long long block_stride, const void *gate, long long gate_stride, void *y,
+                            long long y_stride, void *out, moe_dtype odt, long long out_stride,
+                            float *out_scale, void *stream);
 
 /*
  * MOE_PATH_AUTO's choice for a call of T tokens on this layer (without mask
