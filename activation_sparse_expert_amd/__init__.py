@@ -34,7 +34,7 @@ EXPORTED = ["moe_route_topk", "moe_expert_forward_sparse", "moe_layer_forward",
             "moe_noalloc_scratch_bytes", "moe_materialize_up", "moe_transpose_down",
             "moe_auto_dense_min", "moe_mixed_dense_min", "moe_layer_forward_few",
             "moe_linear_forward", "moe_linear_plan", "moe_linear_q8_forward", "moe_quantize_rows",
-            "moe_dequantize_rows", "moe_norm_forward"]
+            "moe_dequantize_rows", "moe_norm_forward", "moe_linear_q8_plan"]
 
 
 class MoeError(RuntimeError):
@@ -149,6 +149,8 @@ def lib():
         N = C.c_longlong
         L.moe_linear_q8_forward.restype = I
         L.moe_linear_q8_forward.argtypes = [C.POINTER(LinearQ8Desc), P, I, N, P, I, P, N, P, I, N, P, Z, P]
+        L.moe_linear_q8_plan.restype = I
+        L.moe_linear_q8_plan.argtypes = [I, I, I, I, C.POINTER(I), C.POINTER(I)]
         L.moe_quantize_rows.restype = I
         L.moe_quantize_rows.argtypes = [P, I, N, I, I, P, N, P, P]
         L.moe_dequantize_rows.restype = I
@@ -548,8 +550,17 @@ def linear_forward(linear: Linear, x, *, residual=None, y=None, out_dtype=None, 
 def linear_plan(T: int, k: int, n: int, gated: bool = False):
     """How linear_forward cuts a call of these sizes: ((tokens, weight rows) of a tile,
     parts of k), or (None, 0) where it streams the weights past the tokens."""
+    return _plan(lib().moe_linear_plan, T, k, n, gated)
+
+
+def linear_q8_plan(T: int, k: int, n: int, gated: bool = False):
+    """linear_plan of linear_q8_forward."""
+    return _plan(lib().moe_linear_q8_plan, T, k, n, gated)
+
+
+def _plan(fn, T, k, n, gated):
     tokens, rows = C.c_int(), C.c_int()
-    parts = lib().moe_linear_plan(T, k, n, int(gated), C.byref(tokens), C.byref(rows))
+    parts = fn(T, k, n, int(gated), C.byref(tokens), C.byref(rows))
     if parts < 0:
         raise ValueError(f"the linear layer does not take T = {T}, k = {k}, n = {n}")
     return ((tokens.value, rows.value) if parts else None), parts

@@ -1110,6 +1110,15 @@ moe_status moe_linear_q8_forward(const moe_linear_q8 *L, const void *x, moe_dtyp
     return hip_status(launch_linear_q8(a, s));
 }
 
+int moe_linear_q8_plan(int T, int k, int n, int gated, int *tokens, int *rows)
+{
+    int bm = 0, bn = 0, parts = -1;
+    if (linear_q8_size_ok(T, k, n)) parts = linear_q8_parts(T, k, n, gated != 0, &bm, &bn);
+    if (tokens) *tokens = bm;
+    if (rows) *rows = bn;
+    return parts;
+}
+
 moe_status moe_quantize_rows(const void *x, moe_dtype xdt, long long x_stride, int T, int k, int8_t *q,
                              long long q_stride, float *scale, void *stream)
 {

@@ -2,9 +2,15 @@
 #pragma once
 #include "linear.hpp"
 #include "mfma_stream.hpp"
+#include "rows.hpp"
+
+#include <type_traits>
 
 namespace moeffn {
 namespace le {
+
+template <int U>
+using Args = std::conditional_t<U == st::kI8, LinearQ8Args, LinearArgs>;
 
 // v sigmoid(z) with the hardware reciprocal (one unit in the last place, which an
 // fp32 division would cost ten instructions to remove)
@@ -58,8 +64,11 @@ __device__ __forceinline__ void finish(const LinearArgs &p, int t, int n, float 
 }
 
 // Whether four outputs of a token can be read and written together (finish4)
-inline bool quads(const LinearArgs &p)
+template <int U>
+bool quads(const Args<U> &p)
 {
+    if constexpr (U == st::kI8)
+        if ((((uintptr_t)p.sw | (uintptr_t)p.sg) & 15) != 0) return false;
     const size_t al = p.ydt == 2 ? 16 : 8;
     auto ok = [&](const void *q, long long stride) { return ((uintptr_t)q & (al - 1)) == 0 && stride % 4 == 0; };
     return p.N % 4 == 0 && ok(p.y, p.ys) && (!p.r || ok(p.r, p.rs)) && ((uintptr_t)p.b & 15) == 0 &&
@@ -105,6 +114,55 @@ __device__ __forceinline__ void finish4(const LinearArgs &p, int t, int n, float
         }
         *(float4 *)((float *)p.y + at) = make_float4(v[0], v[1], v[2], v[3]);
     }
+}
+
+// The same from sums of the matrix instructions: of 16-bit products as they are, of codes as
+// integers times the token's and the output's scale, the latter first (a weight's scale
+// is far from the ends of fp32).
+template <int U, class S>
+__device__ __forceinline__ void finish_sum(const Args<U> &p, int t, int n, S a, S g)
+{
+    if constexpr (U == st::kI8) {
+        const float sx = p.sx[t];
+        finish(p, t, n, (float)a * p.sw[n] * sx, p.wg ? (float)g * p.sg[n] * sx : 0.f);
+    } else {
+        finish(p, t, n, a, g);
+    }
+}
+
+// Sums that pass through LDS or the workspace as the bits of a float
+__device__ __forceinline__ float bits(float v) { return v; }
+__device__ __forceinline__ float bits(int v) { return __int_as_float(v); }
+
+template <int U>
+__device__ __forceinline__ float add_bits(float a, float b)
+{
+    if constexpr (U == st::kI8) return __int_as_float(__float_as_int(a) + __float_as_int(b));
+    else return a + b;
+}
+
+template <int U>
+__device__ __forceinline__ void finish_bits(const Args<U> &p, int t, int n, float a, float g)
+{
+    if constexpr (U == st::kI8) finish_sum<U>(p, t, n, __float_as_int(a), __float_as_int(g));
+    else finish(p, t, n, a, g);
+}
+
+template <int U>
+__device__ __forceinline__ void finish_bits4(const Args<U> &p, int t, int n, float (&v)[4], float (&g)[4])
+{
+    if constexpr (U == st::kI8) {
+        const float sx = p.sx[t];
+        const float4 w = *(const float4 *)(p.sw + n);
+        v[0] = (float)__float_as_int(v[0]) * w.x * sx; v[1] = (float)__float_as_int(v[1]) * w.y * sx;
+        v[2] = (float)__float_as_int(v[2]) * w.z * sx; v[3] = (float)__float_as_int(v[3]) * w.w * sx;
+        if (p.wg) {
+            const float4 s = *(const float4 *)(p.sg + n);
+            g[0] = (float)__float_as_int(g[0]) * s.x * sx; g[1] = (float)__float_as_int(g[1]) * s.y * sx;
+            g[2] = (float)__float_as_int(g[2]) * s.z * sx; g[3] = (float)__float_as_int(g[3]) * s.w * sx;
+        }
+    }
+    finish4(p, t, n, v, g);
 }
 
 }  // namespace le

@@ -1,51 +1,47 @@
-// Linear layer on 8-bit codes: each wave multiplies 16 weight rows by 16 tokens over all of
-// k with v_mfma_i32_16x16x64_i8 (lane l holds row l % 16, 16 codes at k 16 (l / 16); value r
-// of lane l of the result is row 4 (l / 16) + r, token l % 16).
-#include "linear_epilogue.hpp"
-#include "rows.hpp"
+// Linear layer on 8-bit codes: the 16-bit layer's kernels with two codes in each 16-bit unit
+// (mfma_stream.hpp), so that K, strides and blocks count pairs of codes here.
+#include "linear_stream.hpp"
+#include "linear_tile.hpp"
 
 namespace moeffn {
 
 namespace {
 
-typedef int intx4 __attribute__((ext_vector_type(4)));
-
-__global__ void __launch_bounds__(256)
-linear_q8_kernel(LinearQ8Args a)
+bool q8_streams(int T, int K, int N)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n0 = 16 * (blockIdx.x * 4 + wave), t0 = 16 * blockIdx.y;
-    if (n0 >= a.N) return;
-    const int li = lane & 15, k0 = 16 * (lane >> 4);
-    const int n = min(n0 + li, a.N - 1), t = min(t0 + li, a.T - 1);
-    const int8_t *x = (const int8_t *)a.x + (size_t)t * a.xs;
-    const int8_t *w = (const int8_t *)a.w + (size_t)n * a.K, *wg = (const int8_t *)(a.wg ? a.wg : a.w) + (size_t)n * a.K;
-    intx4 acc = {0, 0, 0, 0}, gate = {0, 0, 0, 0};
-    for (int k = k0; k - k0 < a.K; k += 64) {
-        const intx4 none = {0, 0, 0, 0};
-        const bool in = k < a.K;
-        const intx4 xv = in ? *(const intx4 *)(x + k) : none;
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(in ? *(const intx4 *)(w + k) : none, xv, acc, 0, 0, 0);
-        if (a.wg) gate = __builtin_amdgcn_mfma_i32_16x16x64_i8(in ? *(const intx4 *)(wg + k) : none, xv, gate, 0, 0, 0);
-    }
-    if (t0 + li >= a.T) return;
-    for (int r = 0; r < 4; ++r) {
-        const int j = n0 + 4 * (lane >> 4) + r;
-        if (j >= a.N) break;
-        const float sx = a.sx[t0 + li];
-        le::finish(a, t0 + li, j, (float)acc[r] * a.sw[j] * sx, a.wg ? (float)gate[r] * a.sg[j] * sx : 0.f);
-    }
+    return T <= 32 || (K <= 8192 && (long long)((T + 31) / 32) * ((N + 15) / 16) <= kUnits);
 }
 
 }  // namespace
 
-hipError_t launch_linear_q8(const LinearQ8Args &a, hipStream_t s)
+int linear_q8_parts(int T, int K, int N, bool gated, int *bm, int *bn)
 {
-    // (at most 65536 tokens: 4096 rows of the grid)
-    hipLaunchKernelGGL(linear_q8_kernel, dim3((unsigned)((a.N + 63) / 64), (unsigned)((a.T + 15) / 16)), dim3(256), 0, s, a);
-    return hipGetLastError();
+    K /= 2;
+    if (q8_streams(T, K, N)) return 0;
+    const Plan p = plan(T, K, N, gated);
+    *bm = kTiles[p.tile].bm;
+    *bn = kTiles[p.tile].bn;
+    return p.c.split;
 }
 
-size_t linear_q8_split_bytes(int, int, int) { return 0; }
+size_t linear_q8_split_bytes(int T, int K, int N)
+{
+    K /= 2;
+    if (q8_streams(T, K, N)) return 0;
+    const Plan p = plan(T, K, N, false), g = plan(T, K, N, true);
+    const size_t np = p.c.split > 1 ? p.c.split : 0, ng = g.c.split > 1 ? 2 * g.c.split : 0;
+    return (np > ng ? np : ng) * (size_t)T * N * 4;
+}
+
+hipError_t launch_linear_q8(const LinearQ8Args &given, hipStream_t s)
+{
+    LinearQ8Args a = given;
+    if (a.T < 1 || a.K < 16 || a.K % 16 != 0 || a.N < 1) return hipErrorInvalidValue;
+    a.K /= 2;
+    a.xs /= 2;
+    // (the offsets of a tile's rows have 32 bits)
+    if (q8_streams(a.T, a.K, a.N) || a.xs > kTileStride) return launch_stream<st::kI8>(a, s);
+    return launch_plan<st::kI8>(a, plan(a.T, a.K, a.N, a.wg != nullptr), s);
+}
 
 }  // namespace moeffn

@@ -24,11 +24,33 @@ namespace st {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef int intx4 __attribute__((ext_vector_type(4)));
 
-template <bool BF16>
-__device__ __forceinline__ floatx4 mma16(const uint4 &a, const uint4 &b, const floatx4 &c)
+// What an operand's 16-bit units hold: an fp16 number, a bf16 number or two 8-bit codes.
+// Products of codes are summed in 32-bit integers; everything else about a unit, its place
+// in a fragment included, is the same (a code of lane l's 16 bytes meets the code at the
+// same place of the other operand).
+enum Unit { kF16 = 0, kBF16 = 1, kI8 = 2 };
+
+template <int U>
+struct Sum {
+    typedef floatx4 x4;
+    typedef float floatx16 __attribute__((ext_vector_type(16)));
+    typedef floatx16 x16;
+};
+template <>
+struct Sum<kI8> {
+    typedef intx4 x4;
+    typedef int intx16 __attribute__((ext_vector_type(16)));
+    typedef intx16 x16;
+};
+
+template <int U>
+__device__ __forceinline__ typename Sum<U>::x4 mma16(const uint4 &a, const uint4 &b, const typename Sum<U>::x4 &c)
 {
-    if constexpr (BF16)
+    if constexpr (U == kI8)
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(intx4, a), __builtin_bit_cast(intx4, b), c, 0, 0, 0);
+    else if constexpr (U == kBF16)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                        __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
     else
@@ -75,13 +97,13 @@ __device__ __forceinline__ void wait_copies()
 }
 
 // XR: token rows of a block (1, 2, 4 or a multiple of 8)
-template <int NM, int XR>
+template <int NM, int XR, int U = kF16>
 struct Ring {
     static constexpr int kTok = (XR + 7) / 8;           // copy instructions of tokens
     static constexpr int kCopies = 2 * NM + kTok;       // instructions per block
     static constexpr int kBlock = 2048 * NM + 128 * XR; // bytes
     static constexpr int kFrag = (XR + 15) / 16;        // groups of 16 tokens
-    typedef floatx4 Acc[NM][kFrag];
+    typedef typename Sum<U>::x4 Acc[NM][kFrag];
     typedef const uint16_t *Src[kCopies];
 };
 
@@ -97,11 +119,11 @@ __device__ __forceinline__ int copy_k(int lane) { return 8 * ((lane & 7) ^ (lane
 //   ring:   D blocks of LDS of this wave (wave-uniform)
 // Columns of D past the XR rows repeat some of them; rows and tokens that do not
 // exist may be given as copies of others: their part of D means nothing.
-template <bool BF16, int NM, int XR, int D>
-__device__ __forceinline__ void stream(typename Ring<NM, XR>::Acc &acc, unsigned char *ring,
-                                       typename Ring<NM, XR>::Src &src, int nb, int kl, int lane)
+template <int U, int NM, int XR, int D>
+__device__ __forceinline__ void stream(typename Ring<NM, XR, U>::Acc &acc, unsigned char *ring,
+                                       typename Ring<NM, XR, U>::Src &src, int nb, int kl, int lane)
 {
-    using R = Ring<NM, XR>;
+    using R = Ring<NM, XR, U>;
     static_assert(XR == 1 || XR == 2 || XR == 4 || XR % 8 == 0, "token rows");
     const int li = lane & 15, q = lane >> 4;
     const int kc = copy_k(lane);
@@ -138,7 +160,7 @@ __device__ __forceinline__ void stream(typename Ring<NM, XR>::Acc &acc, unsigned
 #pragma unroll
             for (int m = 0; m < NM; ++m)
 #pragma unroll
-                for (int j = 0; j < R::kFrag; ++j) acc[m][j] = mma16<BF16>(w[m], x[j], acc[m][j]);
+                for (int j = 0; j < R::kFrag; ++j) acc[m][j] = mma16<U>(w[m], x[j], acc[m][j]);
         }
         // the block's reads are done before a copy may fill its place
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

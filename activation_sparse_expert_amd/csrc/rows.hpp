@@ -65,6 +65,8 @@ struct LinearQ8Args : LinearArgs {
     const float *sw, *sg;               // [N] scales of w and wg
 };
 hipError_t launch_linear_q8(const LinearQ8Args &a, hipStream_t s);
+// The parts of K of a call (0: streamed) and its tile
+int linear_q8_parts(int T, int K, int N, bool gated, int *bm, int *bn);
 size_t linear_q8_split_bytes(int T, int K, int N);      // partial products, enough for the plain and the gated call
 
 }  // namespace moeffn

@@ -454,6 +454,9 @@ moe_status moe_linear_q8_forward(const moe_linear_q8 *L, const void *x, moe_dtyp
                                  long long residual_stride, void *y, moe_dtype ydt, long long y_stride,
                                  void *ws, size_t ws_bytes, void *stream);
 
+/* moe_linear_plan of moe_linear_q8_forward (x_stride up to 2^22). */
+int moe_linear_q8_plan(int T, int k, int n, int gated, int *tokens, int *rows);
+
 /*
  * Rows to 8-bit codes: q_ti = round(127 x_ti / a_t), ties to even, scale_t = a_t / 127 in fp32,
  * a_t = max_i |x_ti|; a weight [n][k] has a scale for each output this way, tokens [T][k] one for
