@@ -1,99 +1,175 @@
-// Norms between two blocks: y = rs r + bs g (.) Npost(o), out = Npre(y), one row a workgroup,
-// kept in LDS in fp32.
-#include "codes.hpp"
-#include "mfma_stream.hpp"
+// Norms between two blocks: y = rs r + bs g (.) Npost(o), out = Npre(y).  Bound by HBM: a row
+// is held in registers by the lanes of part of a wave, or by a workgroup, so that each
+// operand is read and written once.
+#include "row_io.hpp"
 #include "rows.hpp"
+
+#include <algorithm>
 
 namespace moeffn {
 
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
-
-__device__ __forceinline__ float block_sum(float v, float *lds)
+// The norm of a row in place, n[c] of whose elements each group of this lane holds.  Where the
+// squares pass fp32 everything is taken of values 2^-80 as large, beside which eps is nothing.
+template <int L, int C, bool WIDE, bool FULL, bool BARE>
+__device__ __forceinline__ void norm_row(float (&v)[C][8], const int (&n)[C], rio::Team<L> &team, const NormArgs &a,
+                                         const void *w, const void *b)
 {
-    v = seg_sum<64>(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int i = 0; i < kWaves; ++i) v += lds[i];
-    return v;
-}
-
-__device__ __forceinline__ uint32_t block_max(uint32_t v, float *lds)
-{
-    for (int s = 32; s > 0; s >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, s));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = __uint_as_float(v);
-    __syncthreads();
-    for (int i = 0; i < kWaves; ++i) v = max(v, __float_as_uint(lds[i]));
-    return v;
-}
-
-// The row's norm in place; each thread touches its own elements only.  Where the squares
-// pass fp32 everything is taken of values 2^-80 as large, beside which eps is nothing.
-__device__ void norm_row(float *row, int d, int layer, float eps, const void *w, const void *b, int wdt, float add, float *lds)
-{
-    float k = 1.f, m = 0.f, ss = 0.f;
-    for (;;) {
-        if (layer) {
-            m = 0.f;
-            for (int i = threadIdx.x; i < d; i += kThreads) m += row[i] * k;
-            m = block_sum(m, lds) / (float)d;
+    rio::Raw<WIDE> wr[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (w) wr[c] = rio::load<WIDE, FULL>(w, a.wdt, 8 * (team.lane() + c * team.lanes()), n[c]);
+    const float inv = 1.f / (float)a.d;
+    float m = 0.f, ss, k = 1.f;
+    auto stats = [&]() {
+        if (a.layer) {
+            float s = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s += v[c][j] * k;           // (past the row's end: 0)
+            m = team.sum(s) * inv;
         }
-        ss = 0.f;
-        for (int i = threadIdx.x; i < d; i += kThreads) ss += (row[i] * k - m) * (row[i] * k - m);
-        ss = block_sum(ss, lds);
-        if (ss < INFINITY || k != 1.f) break;
-        k = 0x1p-80f;
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float e = (FULL ? n[c] > 0 : j < n[c]) ? v[c][j] * k - m : 0.f;
+                s += e * e;
+            }
+        ss = team.sum(s);
+    };
+    stats();
+    if (__any(!(ss < INFINITY))) {
+        k = ss < INFINITY ? 1.f : 0x1p-80f;
+        stats();
     }
-    const float f = 1.f / sqrtf(ss / (float)d + (k == 1.f ? eps : 0.f));
-    for (int i = threadIdx.x; i < d; i += kThreads) {
-        float v = (row[i] * k - m) * f;
-        if (w) v *= st::load_el(w, wdt, i) + add;
-        if (b) v += st::load_el(b, wdt, i);
-        row[i] = v;
+    const float f = __builtin_amdgcn_rsqf(ss * inv + (k == 1.f ? a.eps : 0.f));
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] = (v[c][j] * k - m) * f;
+        if (w) {
+            float x[8];
+            rio::floats<WIDE>(wr[c], a.wdt, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[c][j] *= x[j] + a.add;
+        }
+        if (b) {
+            float x[8];
+            rio::floats<WIDE>(rio::load<WIDE, FULL>(b, a.wdt, 8 * (team.lane() + c * team.lanes()), n[c]), a.wdt, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[c][j] += x[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] = (FULL ? n[c] > 0 : j < n[c]) ? v[c][j] : 0.f;
     }
 }
 
-__global__ void __launch_bounds__(kThreads)
+// L, C: lanes of a row and groups of 8 a lane (row_io.hpp); WIDE: some input has 32 bits; FULL:
+// d is a multiple of 8; BARE: no block
+template <int L, int C, bool WIDE, bool FULL, bool BARE>
+__global__ void __launch_bounds__(L ? 256 : 1024)
 norm_kernel(NormArgs a)
 {
-    extern __shared__ float row[];
-    __shared__ float lds[kWaves];
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        if (a.o) {
-            for (int i = threadIdx.x; i < a.d; i += kThreads) row[i] = st::load_el(a.o, a.odt, (size_t)t * a.os + i);
-            if (a.post) norm_row(row, a.d, a.layer, a.eps, a.pw, a.pb, a.wdt, a.add, lds);
+    __shared__ __align__(16) rio::Slots slots;
+    rio::Team<L> team(&slots);
+    constexpr int G = L ? 256 / (L ? L : 1) : 1;
+    for (long long base = blockIdx.x; base * G < a.T; base += gridDim.x) {
+        const long long t = base * G + team.row();
+        int n[C], at[C];
+        rio::Raw<WIDE> rr[C], orw[C], gr[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            at[c] = 8 * (team.lane() + c * team.lanes());
+            n[c] = t < a.T ? a.d - at[c] : 0;
+            if (!BARE) orw[c] = rio::load<WIDE, FULL>(rio::at(a.o, a.odt, t * a.os), a.odt, at[c], n[c]);
+            if (a.r) rr[c] = rio::load<WIDE, FULL>(rio::at(a.r, a.rdt, t * a.rs), a.rdt, at[c], n[c]);
+            if (!BARE && a.g) gr[c] = rio::load<WIDE, FULL>(rio::at(a.g, a.odt, t * a.gs), a.odt, at[c], n[c]);
         }
-        for (int i = threadIdx.x; i < a.d; i += kThreads) {
-            float v = a.r ? a.rscale * st::load_el(a.r, a.rdt, (size_t)t * a.rs + i) : 0.f;
-            if (a.o) v += a.bscale * (row[i] * (a.g ? st::load_el(a.g, a.odt, (size_t)t * a.gs + i) : 1.f));
-            if (a.y) st::store_el(a.y, a.rdt, (size_t)t * a.ys + i, v);
-            row[i] = v;
+        float v[C][8];
+        if (!BARE) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) rio::floats<WIDE>(orw[c], a.odt, v[c]);
+            if (a.post) norm_row<L, C, WIDE, FULL, BARE>(v, n, team, a, a.pw, a.pb);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (!BARE && a.g) {
+                float g[8];
+                rio::floats<WIDE>(gr[c], a.odt, g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[c][j] *= g[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[c][j] = BARE ? 0.f : a.bscale * v[c][j];
+            if (a.r) {
+                float r[8];
+                rio::floats<WIDE>(rr[c], a.rdt, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[c][j] += a.rscale * r[j];
+            }
+            if (a.y) rio::store<FULL>(rio::at(a.y, a.rdt, t * a.ys), a.rdt, at[c], n[c], v[c]);
         }
         if (!a.out) continue;
-        norm_row(row, a.d, a.layer, a.eps, a.w, a.b, a.wdt, a.add, lds);
+        norm_row<L, C, WIDE, FULL, BARE>(v, n, team, a, a.w, a.b);
         if (a.ndt != 3) {
-            for (int i = threadIdx.x; i < a.d; i += kThreads) st::store_el(a.out, a.ndt, (size_t)t * a.ns + i, row[i]);
+#pragma unroll
+            for (int c = 0; c < C; ++c) rio::store<FULL>(rio::at(a.out, a.ndt, t * a.ns), a.ndt, at[c], n[c], v[c]);
             continue;
         }
         uint32_t most = 0;
-        for (int i = threadIdx.x; i < a.d; i += kThreads) most = max(most, codes::magnitude(row[i]));
-        const codes::Row c = codes::row(block_max(most, lds));
-        for (int i = threadIdx.x; i < a.d; i += kThreads)
-            ((int8_t *)a.out)[(size_t)t * a.ns + i] = (int8_t)codes::code(row[i], c);
-        if (threadIdx.x == 0) a.out_scale[t] = c.scale;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most = rio::umax(most, codes::magnitude(v[c][j]));
+        const codes::Row r = codes::row(team.max(most));
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            int q[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = codes::code(v[c][j], r);
+            rio::store_codes<FULL>((int8_t *)a.out + t * a.ns, at[c], n[c], q);
+        }
+        if (team.lane() == 0 && t < a.T) a.out_scale[t] = r.scale;
     }
+}
+
+template <bool WIDE, bool FULL, bool BARE>
+hipError_t launch(const NormArgs &a, hipStream_t s)
+{
+    const rio::Shape h = rio::shape(a.d, a.T > 256);
+    const int rows = h.lanes ? 256 / h.lanes : 1;
+    const dim3 g((unsigned)std::min<long long>(((long long)a.T + rows - 1) / rows, 1 << 20)), b(h.threads);
+    switch (h.lanes) {
+    case 8: hipLaunchKernelGGL((norm_kernel<8, 1, WIDE, FULL, BARE>), g, b, 0, s, a); break;
+    case 16: hipLaunchKernelGGL((norm_kernel<16, 1, WIDE, FULL, BARE>), g, b, 0, s, a); break;
+    case 32: hipLaunchKernelGGL((norm_kernel<32, 1, WIDE, FULL, BARE>), g, b, 0, s, a); break;
+    case 64: hipLaunchKernelGGL((norm_kernel<64, 1, WIDE, FULL, BARE>), g, b, 0, s, a); break;
+    default:
+        if (h.groups == 1) hipLaunchKernelGGL((norm_kernel<0, 1, WIDE, FULL, BARE>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((norm_kernel<0, 2, WIDE, FULL, BARE>), g, b, 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+template <bool WIDE, bool FULL>
+hipError_t launch_of(const NormArgs &a, hipStream_t s)
+{
+    return a.o ? launch<WIDE, FULL, false>(a, s) : launch<WIDE, FULL, true>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL(norm_kernel, dim3((unsigned)(a.T < 65536 ? a.T : 65536)), dim3(kThreads), a.d * 4, s, a);
-    return hipGetLastError();
+    if (a.d < 1 || a.d > rio::kHeld) return hipErrorInvalidValue;
+    const bool weights = a.w || a.b || a.pw || a.pb;
+    const bool wide = (a.r && a.rdt == 2) || (a.o && a.odt == 2) || (weights && a.wdt == 2);
+    if (wide) return a.d % 8 ? launch_of<true, false>(a, s) : launch_of<true, true>(a, s);
+    return a.d % 8 ? launch_of<false, false>(a, s) : launch_of<false, true>(a, s);
 }
 
 }  // namespace moeffn

@@ -1,0 +1,226 @@
+// Eight neighbouring elements of a row at a time, of any type and at any address: whole
+// groups are loads and stores of 16 bytes (8 for codes), which gfx950 takes at the
+// alignment of an element; a row's last group goes by elements.
+#pragma once
+#include "codes.hpp"
+#include "mfma_stream.hpp"
+
+namespace moeffn {
+namespace rio {
+
+// The bits of 8 elements; WIDE: of any type, else of a 16-bit type
+template <bool WIDE>
+struct Raw {
+    uint4 a;
+};
+template <>
+struct Raw<true> {
+    uint4 a, b;                         // 16-bit types: a alone
+};
+
+// Element i of an array of type dt
+__device__ __forceinline__ const void *at(const void *p, int dt, long long i) { return (const char *)p + (i << (dt == 2 ? 2 : 1)); }
+__device__ __forceinline__ void *at(void *p, int dt, long long i) { return (char *)p + (i << (dt == 2 ? 2 : 1)); }
+
+__device__ __forceinline__ uint4 load16(const void *p)
+{
+    uint4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
+// Elements i .. i + n - 1 (n up to 8, or 8 and more; none if n <= 0), zeros past them.  FULL: no
+// other n than these between 0 and 8.
+template <bool WIDE, bool FULL = false>
+__device__ __forceinline__ Raw<WIDE> load(const void *p, int dt, uint32_t i, int n)
+{
+    Raw<WIDE> r{};
+    if (n >= 8) {
+        if (!WIDE || dt != 2) {
+            r.a = load16((const uint16_t *)p + i);
+        } else if constexpr (WIDE) {
+            r.a = load16((const float *)p + i);
+            r.b = load16((const float *)p + i + 4);
+        }
+    } else if (!FULL && n > 0) {
+        uint32_t v[8] = {};
+        if (!WIDE || dt != 2) {
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (j < n) v[j] = ((const uint16_t *)p)[i + j];
+            r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6]);
+        } else if constexpr (WIDE) {
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+                if (j < n) v[j] = ((const uint32_t *)p)[i + j];
+            r.a = make_uint4(v[0], v[1], v[2], v[3]);
+            r.b = make_uint4(v[4], v[5], v[6], 0);
+        }
+    }
+    return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void halves(const uint4 &a, float (&v)[8])
+{
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = lo16_to_float<BF16>(w[j]);
+        v[2 * j + 1] = hi16_to_float<BF16>(w[j]);
+    }
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void floats(const Raw<WIDE> &r, int dt, float (&v)[8])
+{
+    if constexpr (WIDE)
+        if (dt == 2) {
+            const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+            return;
+        }
+    if (dt == 1) halves<true>(r.a, v);
+    else halves<false>(r.a, v);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pair16(float a, float b)
+{
+    return st::to16<BF16>(a) | (uint32_t)st::to16<BF16>(b) << 16;
+}
+
+template <bool FULL = false>
+__device__ __forceinline__ void store(void *p, int dt, uint32_t i, int n, const float (&v)[8])
+{
+    if (n >= 8) {
+        if (dt == 2) {
+            __builtin_memcpy((float *)p + i, v, 32);
+        } else {
+            const uint4 w = dt == 1 ? make_uint4(pair16<true>(v[0], v[1]), pair16<true>(v[2], v[3]),
+                                                 pair16<true>(v[4], v[5]), pair16<true>(v[6], v[7]))
+                                    : make_uint4(pair16<false>(v[0], v[1]), pair16<false>(v[2], v[3]),
+                                                 pair16<false>(v[4], v[5]), pair16<false>(v[6], v[7]));
+            __builtin_memcpy((uint16_t *)p + i, &w, 16);
+        }
+    } else if (!FULL) {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < n) st::store_el(p, dt, i + j, v[j]);
+    }
+}
+
+template <bool FULL = false>
+__device__ __forceinline__ void store_codes(int8_t *p, uint32_t i, int n, const int (&q)[8])
+{
+    if (n >= 8) {
+        const uint2 w = make_uint2(codes::pack4(q[0], q[1], q[2], q[3]), codes::pack4(q[4], q[5], q[6], q[7]));
+        __builtin_memcpy(p + i, &w, 8);
+    } else if (!FULL) {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < n) p[i + j] = (int8_t)q[j];
+    }
+}
+
+// ---- the lanes of a row ----------------------------------------------------
+// A row is held by L lanes of a wave (8 to 64) or, with L 0, by a whole workgroup of up to 16
+// waves.  There, partial results go through two sets of LDS slots in turn, so that one
+// barrier does: who writes a set again has passed a barrier after everyone read it.
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+template <int S>
+__device__ __forceinline__ uint32_t bfly_max(uint32_t v)
+{
+    if constexpr (S == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return umax(r[0], r[1]);
+    } else if constexpr (S == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return umax(r[0], r[1]);
+    } else {
+        return umax(v, __float_as_uint(xor_lane<S>(__uint_as_float(v))));
+    }
+}
+template <int SEG, int S = SEG / 2>
+__device__ __forceinline__ uint32_t seg_max(uint32_t v)
+{
+    if constexpr (S == 0) return v;
+    else return seg_max<SEG, S / 2>(bfly_max<S>(v));
+}
+
+struct Slots {
+    uint32_t v[2][16];
+};
+
+template <int L>
+struct Team {
+    Slots *s;
+    int set;
+
+    __device__ __forceinline__ Team(Slots *slots) : s(slots), set(0)
+    {
+        if constexpr (L == 0) {
+            if (threadIdx.x < 32) ((uint32_t *)s)[threadIdx.x] = 0;     // slots of waves that there are not
+            __syncthreads();
+        }
+    }
+    // this lane's place in the row's lanes, their number, and the rows of a workgroup
+    __device__ __forceinline__ int lane() const { return L ? threadIdx.x & (L - 1) : threadIdx.x; }
+    __device__ __forceinline__ int lanes() const { return L ? L : blockDim.x; }
+    __device__ __forceinline__ int row() const { return L ? threadIdx.x / (L ? L : 1) : 0; }
+
+    __device__ __forceinline__ const uint4 *exchange(uint32_t v)
+    {
+        set ^= 1;
+        if ((threadIdx.x & 63) == 0) s->v[set][threadIdx.x >> 6] = v;
+        __syncthreads();
+        return (const uint4 *)s->v[set];
+    }
+    __device__ __forceinline__ float sum(float v)
+    {
+        if constexpr (L != 0) return seg_sum<L>(v);
+        const uint4 *p = exchange(__float_as_uint(seg_sum<64>(v)));
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 q = p[i];
+            t += (__uint_as_float(q.x) + __uint_as_float(q.y)) + (__uint_as_float(q.z) + __uint_as_float(q.w));
+        }
+        return t;
+    }
+    __device__ __forceinline__ uint32_t max(uint32_t v)
+    {
+        if constexpr (L != 0) return seg_max<L>(v);
+        const uint4 *p = exchange(seg_max<64>(v));
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 q = p[i];
+            t = umax(t, umax(umax(q.x, q.y), umax(q.z, q.w)));
+        }
+        return t;
+    }
+};
+
+constexpr int kHeld = 16384;            // elements of a row that a workgroup's registers hold
+
+// The lanes, threads of a workgroup and groups of 8 a lane for rows of k elements.  A workgroup
+// waits for its loads, then for its sums: one row alone has a lane for each group, for the
+// least latency; of many rows a compute unit holds several, in fewer lanes each.
+struct Shape {
+    int lanes, threads, groups;
+};
+inline Shape shape(int k, bool many)
+{
+    const int n8 = (k + 7) / 8;
+    int l = 8;
+    while (l < n8) l *= 2;
+    if (l <= 64) return {l, 256, 1};
+    const int groups = n8 > 1024 || (many && n8 > 256) ? 2 : 1;
+    return {0, 64 * ((n8 + 64 * groups - 1) / (64 * groups)), groups};
+}
+
+}  // namespace rio
+}  // namespace moeffn
