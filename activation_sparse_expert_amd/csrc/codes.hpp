@@ -7,8 +7,9 @@
 // a quotient that fp32 holds comes out exactly, ties (n + 1/2) among them; any other
 // quotient is at least 2^-19 of itself away from a tie, far more than its error.  So
 // the codes of 16-bit rows are those of exact arithmetic.  32-bit rows take the same
-// steps in 64 bits (24 + 7 bits).  The row is first scaled by the power of two that puts
-// max|x| in [1, 2): nothing overflows, and what underflows has the code 0.
+// steps in 64 bits (24 + 7 bits).  Both p and max|x| carry the power of two that puts max|x| in
+// [1, 2) (that of 2^-100 for smaller ones): nothing overflows, and what underflows has the
+// code 0.  The quotient is rounded by adding 1.5 2^23, whose last bits then are the code.
 #pragma once
 #include "device.hpp"
 
@@ -17,9 +18,10 @@ namespace codes {
 
 // What a row's codes are made with, from the bits of its largest |x|.
 struct Row {
-    float a, inv;                       // max|x| 2^-e in [1, 2) and its reciprocal (0: the codes are 0)
-    int e;
+    float k;                            // 127 2^-e
+    float a, inv;                       // max|x| 2^-e and its reciprocal (a row of zeros: 1 and 0)
     float scale;                        // max|x| / 127; NaN for a row with an infinity or NaN
+    bool ok;                            // no infinity or NaN: else the codes are 0
 };
 
 // |x| as an integer that orders as |x| does, infinities above the numbers and NaN above those
@@ -27,41 +29,43 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 
 __device__ __forceinline__ Row row(uint32_t most)
 {
-    Row r{1.f, 0.f, 0, 0.f};
+    Row r{0.f, 1.f, 0.f, 0.f, true};
     if (most >= 0x7F800000u) {
         r.scale = __uint_as_float(0x7FC00000u);
+        r.ok = false;
     } else if (most != 0) {
         const float v = __uint_as_float(most);
-        r.e = __builtin_amdgcn_frexp_expf(v) - 1;
-        r.a = __builtin_amdgcn_ldexpf(v, -r.e);
+        const int e = __builtin_amdgcn_frexp_expf(v) - 1, s = e < -100 ? 100 : -e;
+        r.k = __builtin_amdgcn_ldexpf(127.f, s);
+        r.a = __builtin_amdgcn_ldexpf(v, s);
         r.inv = __builtin_amdgcn_rcpf(r.a);
         r.scale = v / 127.f;
     }
     return r;
 }
 
-// Code of a 16-bit x, or of an fp32 one whose own last bits are not exact anyway
-__device__ __forceinline__ int code(float x, const Row &r)
+// A 16-bit x, or an fp32 one whose own last bits are not exact anyway: bits whose last 8 are the code
+__device__ __forceinline__ uint32_t code(float x, const Row &r)
 {
-    const float p = __builtin_amdgcn_ldexpf(x, -r.e) * 127.f;
-    const float c = p * r.inv;
-    const float q = fmaf(fmaf(-c, r.a, p), r.inv, c);
-    return r.inv != 0.f ? (int)__builtin_rintf(q) : 0;
+    const float p = x * r.k, c = p * r.inv;
+    return __float_as_uint(fmaf(fmaf(-c, r.a, p), r.inv, c) + 12582912.f);
 }
 
-// Code of an fp32 x
-__device__ __forceinline__ int code64(float x, const Row &r)
+// An fp32 x
+__device__ __forceinline__ uint32_t code64(float x, const Row &r)
 {
-    const double p = (double)__builtin_amdgcn_ldexpf(x, -r.e) * 127.0, a = r.a, i0 = r.inv;
+    const double p = (double)x * (double)r.k, a = r.a, i0 = r.inv;
     const double inv = fma(fma(-i0, a, 1.0), i0, i0);           // 46 bits
     const double c = p * inv;
-    const double q = fma(fma(-c, a, p), inv, c);
-    return r.inv != 0.f ? (int)__builtin_rint(q) : 0;
+    // (1.5 2^52: the same in 64 bits)
+    return (uint32_t)__builtin_bit_cast(uint64_t, fma(fma(-c, a, p), inv, c) + 6755399441055744.0);
 }
 
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d)
+// The last bytes of four
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    return (a & 0xFF) | (b & 0xFF) << 8 | (c & 0xFF) << 16 | (uint32_t)d << 24;
+    const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0C0C0400u), hi = __builtin_amdgcn_perm(d, c, 0x04000C0Cu);
+    return lo | hi;
 }
 
 }  // namespace codes

@@ -14,12 +14,8 @@ namespace {
 // squares pass fp32 everything is taken of values 2^-80 as large, beside which eps is nothing.
 template <int L, int C, bool WIDE, bool FULL, bool BARE>
 __device__ __forceinline__ void norm_row(float (&v)[C][8], const int (&n)[C], rio::Team<L> &team, const NormArgs &a,
-                                         const void *w, const void *b)
+                                         const void *w, const rio::Raw<WIDE> (&wr)[C], const void *b)
 {
-    rio::Raw<WIDE> wr[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-        if (w) wr[c] = rio::load<WIDE, FULL>(w, a.wdt, 8 * (team.lane() + c * team.lanes()), n[c]);
     const float inv = 1.f / (float)a.d;
     float m = 0.f, ss, k = 1.f;
     auto stats = [&]() {
@@ -77,23 +73,44 @@ norm_kernel(NormArgs a)
     __shared__ __align__(16) rio::Slots slots;
     rio::Team<L> team(&slots);
     constexpr int G = L ? 256 / (L ? L : 1) : 1;
-    for (long long base = blockIdx.x; base * G < a.T; base += gridDim.x) {
-        const long long t = base * G + team.row();
-        int n[C], at[C];
-        rio::Raw<WIDE> rr[C], orw[C], gr[C];
+    int n[C], at[C];
+    rio::Raw<WIDE> rr[C], orw[C], gr[C], wr[C], pwr[C];
+    auto load_row = [&](long long t, bool first) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            at[c] = 8 * (team.lane() + c * team.lanes());
             n[c] = t < a.T ? a.d - at[c] : 0;
             if (!BARE) orw[c] = rio::load<WIDE, FULL>(rio::at(a.o, a.odt, t * a.os), a.odt, at[c], n[c]);
             if (a.r) rr[c] = rio::load<WIDE, FULL>(rio::at(a.r, a.rdt, t * a.rs), a.rdt, at[c], n[c]);
-            if (!BARE && a.g) gr[c] = rio::load<WIDE, FULL>(rio::at(a.g, a.odt, t * a.gs), a.odt, at[c], n[c]);
+            if (!BARE && a.g && (first || a.gs)) gr[c] = rio::load<WIDE, FULL>(rio::at(a.g, a.odt, t * a.gs), a.odt, at[c], n[c]);
         }
+    };
+    long long base = blockIdx.x;
+#pragma unroll
+    for (int c = 0; c < C; ++c) at[c] = 8 * (team.lane() + c * team.lanes());
+    load_row(base * G + team.row(), true);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (!BARE && a.pw) pwr[c] = rio::load<WIDE, FULL>(a.pw, a.wdt, at[c], a.d - at[c]);
+        if (a.w) wr[c] = rio::load<WIDE, FULL>(a.w, a.wdt, at[c], a.d - at[c]);
+    }
+    for (; base * G < a.T; base += gridDim.x) {
+        const long long t = base * G + team.row();
+        const bool live = t < a.T;
+        int m[C];                                   // n of this row (n is the next one's from its loads on)
         float v[C][8];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            m[c] = n[c];
+            if constexpr (C > 1) {
+                rio::stay_packed<WIDE>(wr[c]);
+                if (!BARE) rio::stay_packed<WIDE>(pwr[c]);
+                if (!BARE) rio::stay_packed<WIDE>(gr[c]);
+            }
+        }
         if (!BARE) {
 #pragma unroll
             for (int c = 0; c < C; ++c) rio::floats<WIDE>(orw[c], a.odt, v[c]);
-            if (a.post) norm_row<L, C, WIDE, FULL, BARE>(v, n, team, a, a.pw, a.pb);
+            if (a.post) norm_row<L, C, WIDE, FULL, BARE>(v, m, team, a, a.pw, pwr, a.pb);
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -111,13 +128,18 @@ norm_kernel(NormArgs a)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[c][j] += a.rscale * r[j];
             }
-            if (a.y) rio::store<FULL>(rio::at(a.y, a.rdt, t * a.ys), a.rdt, at[c], n[c], v[c]);
+        }
+        // the next row of these lanes is on its way while this one is finished
+        if ((base + gridDim.x) * G < a.T) load_row(t + (long long)gridDim.x * G, false);
+        if (a.y) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) rio::store<FULL>(rio::at(a.y, a.rdt, t * a.ys), a.rdt, at[c], m[c], v[c]);
         }
         if (!a.out) continue;
-        norm_row<L, C, WIDE, FULL, BARE>(v, n, team, a, a.w, a.b);
+        norm_row<L, C, WIDE, FULL, BARE>(v, m, team, a, a.w, wr, a.b);
         if (a.ndt != 3) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) rio::store<FULL>(rio::at(a.out, a.ndt, t * a.ns), a.ndt, at[c], n[c], v[c]);
+            for (int c = 0; c < C; ++c) rio::store<FULL>(rio::at(a.out, a.ndt, t * a.ns), a.ndt, at[c], m[c], v[c]);
             continue;
         }
         uint32_t most = 0;
@@ -128,21 +150,22 @@ norm_kernel(NormArgs a)
         const codes::Row r = codes::row(team.max(most));
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            int q[8];
+            uint32_t q[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[j] = codes::code(v[c][j], r);
-            rio::store_codes<FULL>((int8_t *)a.out + t * a.ns, at[c], n[c], q);
+            rio::store_codes<FULL>((int8_t *)a.out + t * a.ns, at[c], m[c], q, r.ok);
         }
-        if (team.lane() == 0 && t < a.T) a.out_scale[t] = r.scale;
+        if (team.lane() == 0 && live) a.out_scale[t] = r.scale;
     }
 }
 
 template <bool WIDE, bool FULL, bool BARE>
 hipError_t launch(const NormArgs &a, hipStream_t s)
 {
-    const rio::Shape h = rio::shape(a.d, a.T > 256);
-    const int rows = h.lanes ? 256 / h.lanes : 1;
-    const dim3 g((unsigned)std::min<long long>(((long long)a.T + rows - 1) / rows, 1 << 20)), b(h.threads);
+    // two groups a lane: 4096 x 6144 between norms to 8 bits 47 us against 52, 2048 x 8192 32 against 35;
+    // 4096 x 4096 28 against 28; with 32-bit operands, whose registers then spill, 71 against 42
+    const rio::Shape h = rio::shape(a.d, WIDE || a.T <= 512 ? rio::kGroups : FULL ? 512 : 256);
+    const dim3 g(rio::grid(h, a.T, h.groups == 2 ? 1024 : 2048)), b(h.threads);
     switch (h.lanes) {
     case 8: hipLaunchKernelGGL((norm_kernel<8, 1, WIDE, FULL, BARE>), g, b, 0, s, a); break;
     case 16: hipLaunchKernelGGL((norm_kernel<16, 1, WIDE, FULL, BARE>), g, b, 0, s, a); break;

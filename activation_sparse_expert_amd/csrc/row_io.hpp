@@ -8,6 +8,8 @@
 namespace moeffn {
 namespace rio {
 
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
 // The bits of 8 elements; WIDE: of any type, else of a 16-bit type
 template <bool WIDE>
 struct Raw {
@@ -58,6 +60,14 @@ __device__ __forceinline__ Raw<WIDE> load(const void *p, int dt, uint32_t i, int
         }
     }
     return r;
+}
+
+// Keeps the compiler from unpacking r before a loop, which would hold it in twice the registers
+template <bool WIDE>
+__device__ __forceinline__ void stay_packed(Raw<WIDE> &r)
+{
+    asm volatile("" : "+v"(r.a.x), "+v"(r.a.y), "+v"(r.a.z), "+v"(r.a.w));
+    if constexpr (WIDE) asm volatile("" : "+v"(r.b.x), "+v"(r.b.y), "+v"(r.b.z), "+v"(r.b.w));
 }
 
 template <bool BF16>
@@ -111,16 +121,41 @@ __device__ __forceinline__ void store(void *p, int dt, uint32_t i, int n, const 
     }
 }
 
+// Codes from the bits that codes::code gives, zeros unless ok
 template <bool FULL = false>
-__device__ __forceinline__ void store_codes(int8_t *p, uint32_t i, int n, const int (&q)[8])
+__device__ __forceinline__ void store_codes(int8_t *p, uint32_t i, int n, const uint32_t (&q)[8], bool ok)
 {
+    uint2 w = make_uint2(codes::pack4(q[0], q[1], q[2], q[3]), codes::pack4(q[4], q[5], q[6], q[7]));
+    if (!ok) w = make_uint2(0, 0);
     if (n >= 8) {
-        const uint2 w = make_uint2(codes::pack4(q[0], q[1], q[2], q[3]), codes::pack4(q[4], q[5], q[6], q[7]));
         __builtin_memcpy(p + i, &w, 8);
     } else if (!FULL) {
 #pragma unroll
         for (int j = 0; j < 7; ++j)
-            if (j < n) p[i + j] = (int8_t)q[j];
+            if (j < n) p[i + j] = (int8_t)((j < 4 ? w.x : w.y) >> 8 * (j & 3));
+    }
+}
+
+// The largest |x| of 8 elements, as codes::magnitude; their bits still in a 16-bit type are
+// compared in pairs
+template <bool WIDE>
+__device__ __forceinline__ uint32_t most(const Raw<WIDE> &r, int dt)
+{
+    if constexpr (WIDE) {
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = umax(m, w[j] & 0x7FFFFFFFu);
+        return m;
+    } else {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+        u16x2 m = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[j] & 0x7FFF7FFFu));
+        const uint16_t h = m.x > m.y ? m.x : m.y;
+        return codes::magnitude(dt == 1 ? bf16_bits_to_float(h) : half_bits_to_float(h));
     }
 }
 
@@ -128,8 +163,6 @@ __device__ __forceinline__ void store_codes(int8_t *p, uint32_t i, int n, const 
 // A row is held by L lanes of a wave (8 to 64) or, with L 0, by a whole workgroup of up to 16
 // waves.  There, partial results go through two sets of LDS slots in turn, so that one
 // barrier does: who writes a set again has passed a barrier after everyone read it.
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
 template <int S>
 __device__ __forceinline__ uint32_t bfly_max(uint32_t v)
 {
@@ -204,22 +237,33 @@ struct Team {
     }
 };
 
-constexpr int kHeld = 16384;            // elements of a row that a workgroup's registers hold
+constexpr int kGroups = 1024;           // groups of 8 that a workgroup's lanes hold one each of
+constexpr int kHeld = 2 * 8 * kGroups;  // elements of a row that its registers hold
 
 // The lanes, threads of a workgroup and groups of 8 a lane for rows of k elements.  A workgroup
-// waits for its loads, then for its sums: one row alone has a lane for each group, for the
-// least latency; of many rows a compute unit holds several, in fewer lanes each.
+// waits for its loads, then for its sums: a lane for each group has the least latency;
+// with two groups a lane (rows of more than `two` groups) a compute unit holds more rows.
 struct Shape {
     int lanes, threads, groups;
 };
-inline Shape shape(int k, bool many)
+inline Shape shape(int k, int two)
 {
     const int n8 = (k + 7) / 8;
     int l = 8;
     while (l < n8) l *= 2;
     if (l <= 64) return {l, 256, 1};
-    const int groups = n8 > 1024 || (many && n8 > 256) ? 2 : 1;
+    const int groups = n8 > two ? 2 : 1;
     return {0, 64 * ((n8 + 64 * groups - 1) / (64 * groups)), groups};
+}
+
+// Workgroups for T rows: no more than the chip holds at a time, about `threads` on each of its 256
+// compute units (rows of part of a wave: 16 workgroups), which then take rows one after
+// another, the next one's loads under way.
+inline unsigned grid(const Shape &h, int T, int threads)
+{
+    const long long wgs = h.lanes ? ((long long)T + 256 / h.lanes - 1) / (256 / h.lanes) : T;
+    const long long held = 256ll * (h.lanes ? 16 : threads > h.threads ? threads / h.threads : 1);
+    return (unsigned)(wgs < held ? wgs : held);
 }
 
 }  // namespace rio
