@@ -423,7 +423,7 @@ def _workspace(torch, device, nbytes, ws):
 def _call(torch, device, what, fn, *args):
     """fn(*args, stream) on the device's current stream, with the device current."""
     i = device.index
-    if i == torch.cuda.current_device():
+    if i == torch._C._cuda_getDevice():                 # (a tensor of the device exists: it is initialised)
         st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(i):
@@ -593,9 +593,18 @@ class LinearQ8:
                             _ptr(self.w_gate), _ptr(self.gate_scale), _ptr(self.bias_gate), ACT[self.act])
 
 
-def _row_dt(t) -> int:
+@functools.lru_cache(maxsize=None)
+def _row_dts():
+    """moe_dtype by torch dtype of row operands: those of _dt, and codes."""
     import torch
-    return MOE_I8 if t.dtype == torch.int8 else _dt(t)
+    return {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.int8: MOE_I8}
+
+
+def _row_dt(t) -> int:
+    dt = _row_dts().get(t.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return dt
 
 
 def linear_q8_forward(linear: LinearQ8, x, *, x_scale=None, residual=None, y=None, out_dtype=None, ws=None):
@@ -616,26 +625,34 @@ def linear_q8_forward(linear: LinearQ8, x, *, x_scale=None, residual=None, y=Non
     xdt = _row_dt(x)
     if (x_scale is None) == (xdt == MOE_I8):
         raise ValueError("x_scale comes with int8 codes and with nothing else")
-    _want("x_scale", x_scale, device, (T,), torch.float32)
+    f32, sp, rp, rs = torch.float32, None, None, 0
+    if x_scale is not None:
+        _want("x_scale", x_scale, device, (T,), f32)
+        sp = _ptr(x_scale)
     _want("w", w, device, (n, k), torch.int8)
-    _want("w_scale", linear.w_scale, device, (n,), torch.float32)
-    _want("bias", linear.bias, device, (n,), torch.float32)
+    _want("w_scale", linear.w_scale, device, (n,), f32)
+    if linear.bias is not None:
+        _want("bias", linear.bias, device, (n,), f32)
     if (linear.w_gate is None) != (linear.gate_scale is None):
         raise ValueError("w_gate and gate_scale come together")
-    _want("w_gate", linear.w_gate, device, (n, k), torch.int8)
-    _want("gate_scale", linear.gate_scale, device, (n,), torch.float32)
-    _want("bias_gate", linear.bias_gate, device, (n,), torch.float32)
+    if linear.w_gate is not None:
+        _want("w_gate", linear.w_gate, device, (n, k), torch.int8)
+        _want("gate_scale", linear.gate_scale, device, (n,), f32)
+    if linear.bias_gate is not None:
+        _want("bias_gate", linear.bias_gate, device, (n,), f32)
     if y is None:
-        y = torch.empty((T, n), dtype=out_dtype or torch.float32, device=device)
+        y = torch.empty((T, n), dtype=out_dtype or f32, device=device)
+        yp, ys = y.data_ptr(), n
     else:
         _want("y", y, device, (T, n))
-    _want("residual", residual, device, (T, n), y.dtype)
+        yp, ys = _rows("y", y)
+    if residual is not None:
+        _want("residual", residual, device, (T, n), y.dtype)
+        rp, rs = _rows("residual", residual)
     xp, xs = _rows("x", x, 16)
-    yp, ys = _rows("y", y)
-    rp, rs = _rows("residual", residual) if residual is not None else (None, 0)
     ws, wp, wb = _workspace(torch, device, _size_of(OP_LINEAR_Q8, T, k, n, xdt, 0, 0), ws)
     _call(torch, device, "moe_linear_q8_forward", lib().moe_linear_q8_forward, C.byref(linear.desc()), xp, xdt,
-          xs, _ptr(x_scale), T, rp, rs, yp, _dt(y), ys, wp, wb)
+          xs, sp, T, rp, rs, yp, _row_dt(y), ys, wp, wb)
     return y
 
 
@@ -652,15 +669,16 @@ def quantize_rows(x, *, q=None, scale=None):
     T, k = x.shape
     if q is None:
         q = torch.empty((T, k), dtype=torch.int8, device=device)
+        qp, qs = q.data_ptr(), k
     else:
         _want("q", q, device, (T, k), torch.int8)
+        qp, qs = _rows("q", q)
     if scale is None:
         scale = torch.empty(T, dtype=torch.float32, device=device)
     else:
         _want("scale", scale, device, (T,), torch.float32)
     xp, xs = _rows("x", x)
-    qp, qs = _rows("q", q)
-    _call(torch, device, "moe_quantize_rows", lib().moe_quantize_rows, xp, _dt(x), xs, T, k, qp, qs, _ptr(scale))
+    _call(torch, device, "moe_quantize_rows", lib().moe_quantize_rows, xp, _row_dt(x), xs, T, k, qp, qs, _ptr(scale))
     return q, scale
 
 
@@ -677,11 +695,12 @@ def dequantize_rows(q, scale, *, y=None, out_dtype=None):
     _want("scale", scale, device, (T,), torch.float32)
     if y is None:
         y = torch.empty((T, k), dtype=out_dtype or torch.float32, device=device)
+        yp, ys = y.data_ptr(), k
     else:
         _want("y", y, device, (T, k))
+        yp, ys = _rows("y", y)
     qp, qs = _rows("q", q)
-    yp, ys = _rows("y", y)
-    _call(torch, device, "moe_dequantize_rows", lib().moe_dequantize_rows, qp, qs, _ptr(scale), T, k, yp, _dt(y), ys)
+    _call(torch, device, "moe_dequantize_rows", lib().moe_dequantize_rows, qp, qs, _ptr(scale), T, k, yp, _row_dt(y), ys)
     return y
 
 
@@ -701,14 +720,22 @@ class Norm:
     block_scale: float = 1.0
 
     def desc(self) -> NormDesc:
-        if self.kind not in NORM:
+        kind = NORM.get(self.kind)
+        if kind is None:
             raise ValueError(f"kind must be one of {sorted(NORM)}")
-        given = [t for t in (self.w, self.b, self.post_w, self.post_b) if t is not None]
-        if any(t.dtype != given[0].dtype for t in given):
-            raise TypeError("the norms' weights and biases must have one dtype")
-        return NormDesc(self.d, NORM[self.kind], self.eps, _dt(given[0]) if given else MOE_F32, _ptr(self.w),
-                        _ptr(self.b), int(bool(self.post)), _ptr(self.post_w), _ptr(self.post_b),
-                        int(bool(self.offset)), self.residual_scale, self.block_scale)
+        dtype, at = None, []
+        for t in (self.w, self.b, self.post_w, self.post_b):
+            if t is None:
+                at.append(None)
+                continue
+            if dtype is None:
+                dtype = t.dtype
+            elif t.dtype != dtype:
+                raise TypeError("the norms' weights and biases must have one dtype")
+            at.append(_ptr(t))
+        return NormDesc(self.d, kind, self.eps, MOE_F32 if dtype is None else _row_dts().get(dtype, -1), at[0], at[1],
+                        int(bool(self.post)), at[2], at[3], int(bool(self.offset)), self.residual_scale,
+                        self.block_scale)
 
 
 def norm_forward(norm: Norm, residual, block=None, *, gate=None, y=None, out=None, out_dtype=None, out_scale=None):
@@ -730,47 +757,48 @@ def norm_forward(norm: Norm, residual, block=None, *, gate=None, y=None, out=Non
     device = x.device
     if device.type != "cuda":
         raise ValueError("residual and block must be GPU tensors")
-    T, d = x.shape
-    shape = (T, d)
+    shape = x.shape
+    T, d = shape
     if d != norm.d:
         raise ValueError(f"the rows have {d} columns, the norm d = {norm.d}")
-    for name in ("w", "b", "post_w", "post_b"):
-        t = getattr(norm, name)
-        if t is not None:
-            _want(name, t, device, (d,))
-    rp, rs, bp, bs, gp, gs = None, 0, None, 0, None, 0
+    for t in (norm.w, norm.b, norm.post_w, norm.post_b):
+        if t is not None and (t.device != device or t.shape != (d,)):
+            _want("a norm's weight or bias", t, device, (d,))
+    like = x if block is None else block
+    rp = bp = gp = yp = op = None
+    rs = bs = gs = ys = ns = bdt = odt = 0
     if residual is not None:
         rp, rs = _rows("residual", residual)
     if block is not None:
         _want("block", block, device, shape)
         bp, bs = _rows("block", block)
+        bdt = _row_dt(block)
     if gate is not None:
         if block is None:
             raise ValueError("a gate needs a block")
-        if gate.dim() == 1:
-            _want("gate", gate, device, (d,), block.dtype)
-            gp = _ptr(gate)
-        else:
-            _want("gate", gate, device, shape, block.dtype)
-            gp, gs = _rows("gate", gate)
-    if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=device) if block is not None else False
-    elif y is not False:
+        _want("gate", gate, device, (d,) if gate.dim() == 1 else shape, block.dtype)
+        gp, gs = (_ptr(gate), 0) if gate.dim() == 1 else _rows("gate", gate)
+    if y is None and block is not None:
+        y = torch.empty(shape, dtype=x.dtype, device=device)
+        yp, ys = y.data_ptr(), d
+    elif y is not None and y is not False:
         _want("y", y, device, shape, x.dtype)
+        yp, ys = _rows("y", y)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or (block if block is not None else x).dtype, device=device)
+        out = torch.empty(shape, dtype=out_dtype or like.dtype, device=device)
+        op, ns = out.data_ptr(), d
     elif out is not False:
         _want("out", out, device, shape)
-    yp, ys = _rows("y", y) if y is not False else (None, 0)
-    op, os_ = _rows("out", out) if out is not False else (None, 0)
-    codes = out is not False and out.dtype == torch.int8
-    if codes and out_scale is None:
-        out_scale = torch.empty(T, dtype=torch.float32, device=device)
-    _want("out_scale", out_scale, device, (T,), torch.float32)
-    _call(torch, device, "moe_norm_forward", lib().moe_norm_forward, C.byref(norm.desc()), T, rp, _dt(x), rs, bp,
-          _dt(block) if block is not None else 0, bs, gp, gs, yp, ys, op, _row_dt(out) if op is not None else 0, os_,
-          _ptr(out_scale))
-    return y if y is not False else None, out if out is not False else None, out_scale
+        op, ns = _rows("out", out)
+    if op is not None:
+        odt = _row_dt(out)
+        if odt == MOE_I8 and out_scale is None:
+            out_scale = torch.empty(T, dtype=torch.float32, device=device)
+    if out_scale is not None:
+        _want("out_scale", out_scale, device, (T,), torch.float32)
+    _call(torch, device, "moe_norm_forward", lib().moe_norm_forward, C.byref(norm.desc()), T, rp, _row_dt(x), rs, bp,
+          bdt, bs, gp, gs, yp, ys, op, odt, ns, None if out_scale is None else _ptr(out_scale))
+    return None if y is False else y, None if out is False else out, out_scale
 
 
 def calibrate_threshold(v, q: float, *, out=None, ws=None):
