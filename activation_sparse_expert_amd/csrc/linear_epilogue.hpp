@@ -75,47 +75,6 @@ bool quads(const Args<U> &p)
            ((uintptr_t)p.bg & 15) == 0;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void residual_store4(const LinearArgs &p, size_t at, size_t ar, float (&v)[4])
-{
-    if (p.r) {
-        const uint2 r = *(const uint2 *)((const uint16_t *)p.r + ar);
-        v[0] += lo16_to_float<BF16>(r.x);
-        v[1] += hi16_to_float<BF16>(r.x);
-        v[2] += lo16_to_float<BF16>(r.y);
-        v[3] += hi16_to_float<BF16>(r.y);
-    }
-    *(uint2 *)((uint16_t *)p.y + at) =
-        make_uint2(st::to16<BF16>(v[0]) | (uint32_t)st::to16<BF16>(v[1]) << 16,
-                   st::to16<BF16>(v[2]) | (uint32_t)st::to16<BF16>(v[3]) << 16);
-}
-
-// Outputs n .. n + 3 (n a multiple of 4, all below N) of token t
-__device__ __forceinline__ void finish4(const LinearArgs &p, int t, int n, float (&v)[4], float (&g)[4])
-{
-    if (p.b) {
-        const float4 b = *(const float4 *)(p.b + n);
-        v[0] += b.x; v[1] += b.y; v[2] += b.z; v[3] += b.w;
-    }
-    if (p.bg) {
-        const float4 b = *(const float4 *)(p.bg + n);
-        g[0] += b.x; g[1] += b.y; g[2] += b.z; g[3] += b.w;
-    }
-    values<4>(p, v, g);
-    const size_t at = (size_t)t * p.ys + n, ar = (size_t)t * p.rs + n;
-    if (p.ydt == 1) {
-        residual_store4<true>(p, at, ar, v);
-    } else if (p.ydt == 0) {
-        residual_store4<false>(p, at, ar, v);
-    } else {
-        if (p.r) {
-            const float4 r = *(const float4 *)((const float *)p.r + ar);
-            v[0] += r.x; v[1] += r.y; v[2] += r.z; v[3] += r.w;
-        }
-        *(float4 *)((float *)p.y + at) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-}
-
 // The same from sums of the matrix instructions: of 16-bit products as they are, of codes as
 // integers times the token's and the output's scale, the latter first (a weight's scale
 // is far from the ends of fp32).
@@ -148,21 +107,124 @@ __device__ __forceinline__ void finish_bits(const Args<U> &p, int t, int n, floa
     else finish(p, t, n, a, g);
 }
 
+// What the outputs n .. n + 3 need of their rows of W and Wg: scales and biases.  A lane of a
+// tile's epilogue has the same outputs of many tokens and loads this once.
+struct Cols {
+    float w[4], g[4], b[4], bg[4];
+};
+
+__device__ __forceinline__ void cols4(float (&v)[4], const float *p, int n, int N, bool quads)
+{
+    if (quads) {
+        const float4 q = *(const float4 *)(p + n);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = p[min(n + x, N - 1)];
+    }
+}
+
+template <int U>
+__device__ __forceinline__ void load_cols(const Args<U> &p, Cols &c, int n, bool quads)
+{
+    if constexpr (U == st::kI8) {
+        cols4(c.w, p.sw, n, p.N, quads);
+        if (p.wg) cols4(c.g, p.sg, n, p.N, quads);
+    }
+    if (p.b) cols4(c.b, p.b, n, p.N, quads);
+    if (p.bg) cols4(c.bg, p.bg, n, p.N, quads);
+}
+
+// The residual of four outputs of a token, at ar, before its conversion (m of them exist)
+__device__ __forceinline__ uint4 load_residual(const LinearArgs &p, size_t ar, int m, bool quads)
+{
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (quads) {
+        if (p.ydt == 2) {
+            r = *(const uint4 *)((const float *)p.r + ar);
+        } else {
+            const uint2 q = *(const uint2 *)((const uint16_t *)p.r + ar);
+            r.x = q.x; r.y = q.y;
+        }
+    } else if (p.ydt == 2) {
+        const uint32_t *q = (const uint32_t *)p.r + ar;
+        r = make_uint4(q[0], m > 1 ? q[1] : 0, m > 2 ? q[2] : 0, m > 3 ? q[3] : 0);
+    } else {
+        const uint16_t *q = (const uint16_t *)p.r + ar;
+        r.x = q[0] | (m > 1 ? (uint32_t)q[1] << 16 : 0);
+        r.y = (m > 2 ? q[2] : 0) | (m > 3 ? (uint32_t)q[3] << 16 : 0);
+    }
+    return r;
+}
+
+// Four outputs of a token with scale sx from their sums v (and g) as bits, residual aside; ACT:
+// moe_act, or -1 for p.act
+template <int U, int ACT>
+__device__ __forceinline__ void apply_cols(const Args<U> &p, const Cols &c, float sx, float (&v)[4], float (&g)[4])
+{
+    if constexpr (U == st::kI8) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = (float)__float_as_int(v[x]) * c.w[x] * sx;
+        if (p.wg)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) g[x] = (float)__float_as_int(g[x]) * c.g[x] * sx;
+    }
+    if (p.b)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] += c.b[x];
+    if (p.bg)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) g[x] += c.bg[x];
+    if constexpr (ACT < 0) values<4>(p, v, g);
+    else values_as<4, ACT>(p, v, g);
+}
+
+// Adds the residual's bits r (RES: there is one) and stores; YDT: p.ydt
+template <int YDT, bool RES>
+__device__ __forceinline__ void add_store4(const LinearArgs &p, const uint4 &r, size_t at, int m, bool quads, float (&v)[4])
+{
+    if constexpr (RES) {
+        if constexpr (YDT == 2) {
+            v[0] += __uint_as_float(r.x); v[1] += __uint_as_float(r.y);
+            v[2] += __uint_as_float(r.z); v[3] += __uint_as_float(r.w);
+        } else {
+            v[0] += lo16_to_float<YDT == 1>(r.x); v[1] += hi16_to_float<YDT == 1>(r.x);
+            v[2] += lo16_to_float<YDT == 1>(r.y); v[3] += hi16_to_float<YDT == 1>(r.y);
+        }
+    }
+    if (!quads) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (x < m) st::store_el(p.y, YDT, at + x, v[x]);
+    } else if constexpr (YDT == 2) {
+        *(float4 *)((float *)p.y + at) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        *(uint2 *)((uint16_t *)p.y + at) =
+            make_uint2(st::to16<YDT == 1>(v[0]) | (uint32_t)st::to16<YDT == 1>(v[1]) << 16,
+                       st::to16<YDT == 1>(v[2]) | (uint32_t)st::to16<YDT == 1>(v[3]) << 16);
+    }
+}
+
+// Outputs n .. n + 3 (n a multiple of 4, all below N) of token t
 template <int U>
 __device__ __forceinline__ void finish_bits4(const Args<U> &p, int t, int n, float (&v)[4], float (&g)[4])
 {
-    if constexpr (U == st::kI8) {
-        const float sx = p.sx[t];
-        const float4 w = *(const float4 *)(p.sw + n);
-        v[0] = (float)__float_as_int(v[0]) * w.x * sx; v[1] = (float)__float_as_int(v[1]) * w.y * sx;
-        v[2] = (float)__float_as_int(v[2]) * w.z * sx; v[3] = (float)__float_as_int(v[3]) * w.w * sx;
-        if (p.wg) {
-            const float4 s = *(const float4 *)(p.sg + n);
-            g[0] = (float)__float_as_int(g[0]) * s.x * sx; g[1] = (float)__float_as_int(g[1]) * s.y * sx;
-            g[2] = (float)__float_as_int(g[2]) * s.z * sx; g[3] = (float)__float_as_int(g[3]) * s.w * sx;
-        }
-    }
-    finish4(p, t, n, v, g);
+    Cols c;
+    load_cols<U>(p, c, n, true);
+    float sx = 0.f;
+    if constexpr (U == st::kI8) sx = p.sx[t];
+    uint4 r{};
+    if (p.r) r = load_residual(p, (size_t)t * p.rs + n, 4, true);
+    apply_cols<U, -1>(p, c, sx, v, g);
+    const size_t at = (size_t)t * p.ys + n;
+    auto store = [&](auto res) {
+        constexpr bool R = decltype(res)::value;
+        if (p.ydt == 2) add_store4<2, R>(p, r, at, 4, true, v);
+        else if (p.ydt == 1) add_store4<1, R>(p, r, at, 4, true, v);
+        else add_store4<0, R>(p, r, at, 4, true, v);
+    };
+    if (p.r) store(std::true_type());
+    else store(std::false_type());
 }
 
 }  // namespace le

@@ -86,57 +86,154 @@ __device__ __forceinline__ void copy16_to_lds_at(const void *base, uint32_t off,
 
 // Epilogue of a wave's subtiles (value r of lane l of a subtile is output
 // 8 (r / 4) + 4 (l / 32) + r % 4, token l % 32): 32 tokens at a time through LDS
-// of the wave's own, so that it stores whole runs of a token's outputs.
+// of the wave's own, so that it stores whole runs of a token's outputs.  A lane keeps
+// its four outputs over all tokens, with their scales and biases in registers; the tokens'
+// scales lie in the padding of the LDS rows.
+// A short loop over the 32 tokens, made for one activation, stores the outputs; with a
+// residual it works in LDS alone, and a second pass adds the residual, all of which was
+// loaded before, and stores.
+// A load between the stores would wait for them (they count together), 1200 cycles a
+// time, and unrolled code that runs once waits for its instructions: either way took
+// 5000 cycles a subtile.
 constexpr int kPadRow(int tn) { return 32 * tn + 4; }
 constexpr int kWaveLds(int tn) { return 32 * kPadRow(tn) * 4; }
+
+template <int U, int TN, bool GATED>
+struct StoreTile {
+    static constexpr int HN = GATED ? TN / 2 : TN, LD = kPadRow(TN);
+    static constexpr int kRow = 8 * HN, kStep = 64 / kRow, kIts = 32 / kStep;   // quads of a token, tokens at a time
+    static_assert(64 % kRow == 0, "a lane keeps its outputs");
+    typedef typename st::Sum<U>::x16 Acc;
+
+    const le::Args<U> &a;
+    const Cut &c;
+    int ks, lane, col, n, first, m;                 // m: how many of the lane's four outputs exist
+    bool quads;
+    float *lds;
+    le::Cols cols;
+
+    __device__ __forceinline__ StoreTile(const le::Args<U> &args, const Cut &cut, int run, int n0, int ln, float *l)
+        : a(args), c(cut), ks(run), lane(ln), col(4 * (ln % kRow)), n(n0 + col), first(ln / kRow), m(min(args.N - n, 4)),
+          quads(cut.quads != 0), lds(l)
+    {
+        if (c.split == 1 && m > 0) le::load_cols<U>(a, cols, n, quads);
+    }
+    template <int TM>
+    __device__ __forceinline__ void all(const Acc (&acc)[TM][TN], int t0)
+    {
+        float sx[TM] = {};
+        if constexpr (U == st::kI8)
+            if (c.split == 1)
+#pragma unroll
+                for (int i = 0; i < TM; ++i) sx[i] = a.sx[min(t0 + 32 * i + (lane & 31), a.T - 1)];
+        from<0>(acc, sx, t0);
+    }
+    // subtile row I and those after it (a template: acc has to stay in registers)
+    template <int I, int TM>
+    __device__ __forceinline__ void from(const Acc (&acc)[TM][TN], const float (&sx)[TM], int t0)
+    {
+        if constexpr (I < TM) {
+            uint4 r[kIts];
+            if (a.r && c.split == 1)
+#pragma unroll
+                for (int it = 0; it < kIts; ++it) {
+                    const int tok = t0 + first + kStep * it;
+                    r[it] = make_uint4(0, 0, 0, 0);
+                    if (m > 0 && tok < a.T) r[it] = le::load_residual(a, (size_t)tok * a.rs + n, m, quads);
+                }
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *(float4 *)&lds[(lane & 31) * LD + 32 * j + 8 * q + 4 * (lane >> 5)] =
+                        make_float4(le::bits(acc[I][j][4 * q]), le::bits(acc[I][j][4 * q + 1]),
+                                    le::bits(acc[I][j][4 * q + 2]), le::bits(acc[I][j][4 * q + 3]));
+            if constexpr (U == st::kI8)
+                if (lane < 32) lds[lane * LD + 32 * TN] = sx[I];
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");         // written by other lanes of this wave
+            if (c.split > 1) {
+                parts(t0);
+            } else {
+                if (a.act == 1) apply<1>(t0);
+                else if (a.act == 2) apply<2>(t0);
+                else if (a.act == 3) apply<3>(t0);
+                else if (a.act == 4) apply<4>(t0);
+                else apply<0>(t0);
+                if (!a.r) {
+                } else if (a.ydt == 2) emit<2>(t0, r);
+                else if (a.ydt == 1) emit<1>(t0, r);
+                else emit<0>(t0, r);
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");         // read before the next 32 tokens are written
+            from<I + 1>(acc, sx, t0 + 32);
+        }
+    }
+    __device__ __forceinline__ void sums(int t, float (&v)[4], float (&g)[4])
+    {
+        const float4 v4 = *(const float4 *)&lds[t * LD + col];
+        const float4 g4 = *(const float4 *)&lds[t * LD + col + (GATED ? 32 * HN : 0)];
+        v[0] = v4.x; v[1] = v4.y; v[2] = v4.z; v[3] = v4.w;
+        g[0] = g4.x; g[1] = g4.y; g[2] = g4.z; g[3] = g4.w;
+    }
+    // Outputs of the 32 tokens, stored if there is no residual, else back to LDS
+    template <int ACT>
+    __device__ __forceinline__ void apply(int t0)
+    {
+#pragma unroll 1
+        for (int t = first; t < 32; t += kStep) {
+            float v[4], g[4];
+            sums(t, v, g);
+            le::apply_cols<U, ACT>(a, cols, lds[t * LD + 32 * TN], v, g);
+            const size_t at = (size_t)(t0 + t) * a.ys + n;
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            if (a.r) *(float4 *)&lds[t * LD + col] = make_float4(v[0], v[1], v[2], v[3]);
+            else if (m <= 0 || t0 + t >= a.T) continue;
+            else if (a.ydt == 2) le::add_store4<2, false>(a, none, at, m, quads, v);
+            else if (a.ydt == 1) le::add_store4<1, false>(a, none, at, m, quads, v);
+            else le::add_store4<0, false>(a, none, at, m, quads, v);
+        }
+    }
+    template <int YDT>
+    __device__ __forceinline__ void emit(int t0, const uint4 (&r)[kIts])
+    {
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+            const int t = first + kStep * it, tok = t0 + t;
+            const float4 q = *(const float4 *)&lds[t * LD + col];       // (this lane's own)
+            float v[4] = {q.x, q.y, q.z, q.w};
+            if (m > 0 && tok < a.T) le::add_store4<YDT, true>(a, r[it], (size_t)tok * a.ys + n, m, quads, v);
+        }
+    }
+    __device__ __forceinline__ void parts(int t0)
+    {
+        const size_t plane = (size_t)a.T * a.N;
+#pragma unroll 1
+        for (int t = first; t < 32; t += kStep) {
+            const int tok = t0 + t;
+            if (m <= 0 || tok >= a.T) break;
+            float v[4], g[4];
+            sums(t, v, g);
+            float *p = a.part + (size_t)ks * (GATED ? 2 : 1) * plane + (size_t)tok * a.N + n;
+            if (quads) {
+                *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]);
+                if (GATED) *(float4 *)(p + plane) = make_float4(g[0], g[1], g[2], g[3]);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (x < m) {
+                        p[x] = v[x];
+                        if (GATED) p[plane + x] = g[x];
+                    }
+            }
+        }
+    }
+};
 
 template <int U, int TM, int TN, bool GATED>
 __device__ __forceinline__ void store_tile(const le::Args<U> &a, const Cut &c, int ks, int t0, int n0, int lane,
                                            float *lds, const typename st::Sum<U>::x16 (&acc)[TM][TN])
 {
-    constexpr int HN = GATED ? TN / 2 : TN, LD = kPadRow(TN);
-    const size_t plane = (size_t)a.T * a.N;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *(float4 *)&lds[(lane & 31) * LD + 32 * j + 8 * q + 4 * (lane >> 5)] =
-                    make_float4(le::bits(acc[i][j][4 * q]), le::bits(acc[i][j][4 * q + 1]), le::bits(acc[i][j][4 * q + 2]),
-                                le::bits(acc[i][j][4 * q + 3]));
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // written by other lanes of this wave
-#pragma unroll 1
-        for (int e = lane; e < 32 * 8 * HN; e += 64) {
-            const int t = e / (8 * HN), col = 4 * (e % (8 * HN)), n = n0 + col;
-            const float4 v4 = *(const float4 *)&lds[t * LD + col];
-            const float4 g4 = *(const float4 *)&lds[t * LD + col + (GATED ? 32 * HN : 0)];
-            float v[4] = {v4.x, v4.y, v4.z, v4.w}, g[4] = {g4.x, g4.y, g4.z, g4.w};
-            const int tok = t0 + 32 * i + t;
-            if (tok >= a.T || n >= a.N) continue;
-            if (c.split > 1) {
-                float *p = a.part + (size_t)ks * (GATED ? 2 : 1) * plane + (size_t)tok * a.N + n;
-                if (c.quads) {
-                    *(float4 *)p = v4;
-                    if (GATED) *(float4 *)(p + plane) = g4;
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (n + x < a.N) {
-                            p[x] = v[x];
-                            if (GATED) p[plane + x] = g[x];
-                        }
-                }
-            } else if (c.quads) {
-                le::finish_bits4<U>(a, tok, n, v, g);
-            } else {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (n + x < a.N) le::finish_bits<U>(a, tok, n + x, v[x], g[x]);
-            }
-        }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");     // read before the next 32 tokens are written
-    }
+    StoreTile<U, TN, GATED>(a, c, ks, n0, lane, lds).all(acc, t0);
 }
 
 // S stages.  While block kb is multiplied the fragments of block kb + 1 are read
