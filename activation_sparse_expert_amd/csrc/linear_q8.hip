@@ -1,5 +1,12 @@
 // Linear layer on 8-bit codes: the 16-bit layer's kernels with two codes in each 16-bit unit
 // (mfma_stream.hpp), so that K, strides and blocks count pairs of codes here.
+// A block of 128 bytes takes the matrix core as long as one of 16-bit numbers (35 cycles a
+// 32x32x32 instruction) and holds twice the k, so that what a block costs beside its MFMAs
+// weighs twice as much: 64 x 128 and 128 x 128 tiles by 8 waves, two on a SIMD, which the
+// 16-bit layer does without.  Measured: 300 x 4096 x 4096 17.5 us (64 x 64 by 4 waves 18.4,
+// 128 x 256 in four parts of K 21.4), 1024 x 4096 x 4096 26.7 (128 x 128 by 4 waves 36, 128 x 64
+// 32.7), 4096 x 4096 x (2 x 14336) 457-461, 2.1 POP/s, where the matrix cores alone reach 3.4
+// on such codes (power) and 4.4 on zeros.
 #include "linear_stream.hpp"
 #include "linear_tile.hpp"
 
@@ -7,6 +14,29 @@ namespace moeffn {
 
 namespace {
 
+constexpr Tile kList[] = {{64, 64, 0.36, 0.50, 3.5}, {64, 128, 0.44, 0.84, 3.5}, {128, 128, 0.70, 0.0, 4.5},
+                          {128, 256, 1.08, 0.0, 6.0}, {256, 256, 2.0, 0.0, 8.0}};
+constexpr Tiles kTiles{kList, 5, 3.0, 8e-6 / 5.0};
+
+hipError_t launch_t(const LinearQ8Args &a, const Plan &p, hipStream_t s)
+{
+    constexpr int U = st::kI8;
+    switch (p.tile) {
+    case 0:
+        return a.wg ? launch_tile<U, 64, 64, 2, 1, true, 4>(a, p.c, s) : launch_tile<U, 64, 64, 2, 2, false, 4>(a, p.c, s);
+    case 1:
+        return a.wg ? launch_tile<U, 64, 128, 2, 2, true, 3>(a, p.c, s)
+                    : launch_tile<U, 64, 128, 2, 4, false, 3>(a, p.c, s);
+    case 2:
+        return a.wg ? launch_tile<U, 128, 128, 4, 2, true, 3>(a, p.c, s)
+                    : launch_tile<U, 128, 128, 4, 2, false, 3>(a, p.c, s);
+    case 3:
+        return a.wg ? launch_big<U, true, 128, 3>(a, p.c, s) : launch_big<U, false, 128, 3>(a, p.c, s);
+    }
+    return a.wg ? launch_big<U, true, 256, 2>(a, p.c, s) : launch_big<U, false, 256, 2>(a, p.c, s);
+}
+
+// As the 16-bit layer: up to 32 tokens, and small products of a workgroup a compute unit
 bool q8_streams(int T, int K, int N)
 {
     return T <= 32 || (K <= 8192 && (long long)((T + 31) / 32) * ((N + 15) / 16) <= kUnits);
@@ -18,9 +48,9 @@ int linear_q8_parts(int T, int K, int N, bool gated, int *bm, int *bn)
 {
     K /= 2;
     if (q8_streams(T, K, N)) return 0;
-    const Plan p = plan(T, K, N, gated);
-    *bm = kTiles[p.tile].bm;
-    *bn = kTiles[p.tile].bn;
+    const Plan p = plan(kTiles, T, K, N, gated);
+    *bm = kList[p.tile].bm;
+    *bn = kList[p.tile].bn;
     return p.c.split;
 }
 
@@ -28,7 +58,7 @@ size_t linear_q8_split_bytes(int T, int K, int N)
 {
     K /= 2;
     if (q8_streams(T, K, N)) return 0;
-    const Plan p = plan(T, K, N, false), g = plan(T, K, N, true);
+    const Plan p = plan(kTiles, T, K, N, false), g = plan(kTiles, T, K, N, true);
     const size_t np = p.c.split > 1 ? p.c.split : 0, ng = g.c.split > 1 ? 2 * g.c.split : 0;
     return (np > ng ? np : ng) * (size_t)T * N * 4;
 }
@@ -41,7 +71,7 @@ hipError_t launch_linear_q8(const LinearQ8Args &given, hipStream_t s)
     a.xs /= 2;
     // (the offsets of a tile's rows have 32 bits)
     if (q8_streams(a.T, a.K, a.N) || a.xs > kTileStride) return launch_stream<st::kI8>(a, s);
-    return launch_plan<st::kI8>(a, plan(a.T, a.K, a.N, a.wg != nullptr), s);
+    return launch_plan<st::kI8>(a, plan(kTiles, a.T, a.K, a.N, a.wg != nullptr), launch_t, s);
 }
 
 }  // namespace moeffn

@@ -79,18 +79,29 @@ linear_stream_kernel(le::Args<U> a, int P, int slice)
     }
 }
 
+constexpr int kLds = 160 * 1024, kStreamUnits = 256;        // of a compute unit; compute units
+
+// Whether `waves` keep HBM busy: 6 to a compute unit, or most of those whose rings fit
+bool plenty(long long waves, int ring)
+{
+    return waves >= 6 * kStreamUnits || 8 * waves >= 7ll * kStreamUnits * (kLds / ring);
+}
+
 template <int U, bool GATED, int NM, int XR, int D>
 hipError_t launch_one(const le::Args<U> &a, hipStream_t s)
 {
-    using R = st::Ring<NM, XR, U>;
+    using R = st::Ring<NM, XR>;
     constexpr int NO = GATED ? NM / 2 : NM;
     const int units = (a.N + 16 * NO - 1) / (16 * NO), blocks = (a.K + 63) / 64;
     constexpr int ring = D * R::kBlock, red = NM * R::kFrag * 1024, per = ring > red ? ring : red;
-    static_assert(4 * per <= 160 * 1024, "four waves' rings fit a compute unit");
+    static_assert(4 * per <= kLds, "four waves' rings fit a compute unit");
     // slices of K: 4; 8 while the waves are too few to fill the chip, a slice
     // keeps 4 blocks and the rings fit; fewer when K is short
     int P = 4;
-    if (8 * per <= 160 * 1024 && (long long)units * P < 2048 && blocks >= 8 * P) P = 8;
+    if (8 * per <= kLds && (long long)units * P < 2048 && blocks >= 8 * P) P = 8;
+    // 2 where those are enough, codes only: their sums do not depend on it (1 x 4096 x 28672
+    // 20.3 us against 21.4, 16 tokens 21.1 against 22.3)
+    if (U == st::kI8 && plenty(2ll * units, per)) P = 2;
     while (P > 1 && blocks < P) P /= 2;
     const int G = P < 4 ? 4 / P : 1, slice = (blocks + P - 1) / P;
     const int lds = G * P * per;
@@ -110,9 +121,13 @@ hipError_t launch_one(const le::Args<U> &a, hipStream_t s)
 template <int U, int XR>
 hipError_t launch_xr(const le::Args<U> &a, hipStream_t s)
 {
-    if constexpr (XR > 16)
-        if (a.N >= 16384)
+    if constexpr (XR > 16) {
+        // (codes, 32 x 4096 x 28672: 24.8 us by 32 + 32 rows, 27.7 by 16 + 16)
+        const int outputs = a.wg ? 32 : 64;
+        const bool wide = U == st::kI8 ? plenty(2ll * (a.N / outputs), 3 * st::Ring<4, XR>::kBlock) : a.N >= 16384;
+        if (wide)
             return a.wg ? launch_one<U, true, 4, XR, 3>(a, s) : launch_one<U, false, 4, XR, 3>(a, s);
+    }
     constexpr int D = XR <= 16 ? 4 : 3;
     return a.wg ? launch_one<U, true, 2, XR, 3>(a, s) : launch_one<U, false, 1, XR, D>(a, s);
 }

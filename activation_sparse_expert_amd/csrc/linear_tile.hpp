@@ -11,8 +11,8 @@
 // Two kernels.  Large products take 256 x 256 or 128 x 256 tiles and 8 waves in two
 // groups a phase apart (linear_big_kernel), the others smaller tiles
 // (linear_tile_kernel); where those are few, K is split over workgroups, whose
-// fp32 products a second kernel adds in a fixed order before the epilogue.
-// plan() chooses by what each was measured to cost.
+// products (fp32, or 32-bit integers of codes) a second kernel adds in a fixed order
+// before the epilogue.  plan() chooses by what each was measured to cost.
 // 4096 x 4096 x (2 x 14336), gated: 780-850 us, 1130-1230 TFLOP/s (MFMA busy 62%
 // of the cycles at the 1.75 GHz that the power limit leaves).  300 x 4096 x 4096:
 // 22 us in 128 x 256 tiles and 4 parts of K, and 5.6 us for their sum: 16 blocks of
@@ -547,35 +547,39 @@ linear_join_kernel(le::Args<U> a, int split)
     }
 }
 
-// The tiles that a call can take, and what a block of 64 k costs a compute unit, in
-// microseconds as measured: one workgroup alone on it, and two together where
-// two fit.  (Alone, a small tile waits: for its barrier, LDS and a chain of MFMAs.
-// 128 x 256 costs 0.88 on a few units and 1.02 with all of them at work.)
+// A tile that a call can take, and what it costs a compute unit, in microseconds as measured: a
+// block of 128 bytes of k for one workgroup alone on the unit and for two together where
+// two fit, and the start and end of a workgroup.  (Alone, a small tile waits: for its
+// barrier, LDS and a chain of MFMAs.)
 struct Tile {
     int bm, bn;                                     // tokens x weight rows
     double one, two;                                // two: 0 where one workgroup's LDS fills the unit
+    double ends;
 };
-constexpr Tile kTiles[] = {{64, 64, 0.40, 0.55}, {128, 64, 0.50, 0.75}, {128, 128, 1.05, 1.25}, {128, 256, 1.0, 0.0},
-                           {256, 256, 1.75, 0.0}};
+// ... and a split of K: the second kernel, and a float of a product written and read
+struct Tiles {
+    const Tile *t;
+    int n;
+    double join, part;
+};
 constexpr int kUnits = 256;                         // compute units
 
 struct Plan {
-    int tile;                                       // of kTiles
+    int tile;                                       // of Tiles
     Cut c;
 };
 
 constexpr long long kTileStride = 1 << 21;          // elements: 256 rows within 1 GB
 
 // The tile and split of K with the least expected time: rounds of workgroups over the
-// compute units, and for a split the second kernel (4 us) and the products written
-// and read at 4 TB/s.
-Plan plan(int T, int K, int N, bool gated)
+// compute units, and the second kernel of a split.
+inline Plan plan(const Tiles &tiles, int T, int K, int N, bool gated)
 {
     const int nkb = (K + kKB - 1) / kKB, g = gated ? 2 : 1;
     Plan best{};
     double least = 1e30;
-    for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
-        const Tile &t = kTiles[i];
+    for (int i = 0; i < tiles.n; ++i) {
+        const Tile &t = tiles.t[i];
         Cut c{};
         c.tm = (T + t.bm - 1) / t.bm;
         c.tn = (N + t.bn / g - 1) / (t.bn / g);
@@ -590,7 +594,8 @@ Plan plan(int T, int K, int N, bool gated)
             if (rest > kUnits) us += t.two;
             else if (rest > 0) us += t.one;
             us *= c.blocks;
-            if (c.split > 1) us += 4.0 + 8e-6 * c.split * g * (double)T * N / 4.0;
+            us += (double)((wgs + per - 1) / per) * t.ends;
+            if (c.split > 1) us += tiles.join + tiles.part * c.split * g * (double)T * N;
             if (us < least) {
                 least = us;
                 best = Plan{i, c};
@@ -626,31 +631,12 @@ hipError_t launch_big(const le::Args<U> &a, const Cut &c, hipStream_t s)
     return launch_cut<U>((const void *)linear_big_kernel<U, GATED, BM, S>, a, c, 512, S * (BM + 256) * 128, s);
 }
 
-template <int U>
-hipError_t launch_t(const le::Args<U> &a, const Plan &p, hipStream_t s)
-{
-    switch (p.tile) {
-    case 0:
-        return a.wg ? launch_tile<U, 64, 64, 2, 1, true, 4>(a, p.c, s)
-                    : launch_tile<U, 64, 64, 2, 2, false, 4>(a, p.c, s);
-    case 1:
-        return a.wg ? launch_tile<U, 128, 64, 4, 1, true, 3>(a, p.c, s)
-                    : launch_tile<U, 128, 64, 2, 2, false, 3>(a, p.c, s);
-    case 2:
-        return a.wg ? launch_tile<U, 128, 128, 2, 2, true, 2>(a, p.c, s)
-                    : launch_tile<U, 128, 128, 2, 2, false, 2>(a, p.c, s);
-    case 3:
-        return a.wg ? launch_big<U, true, 128, 3>(a, p.c, s) : launch_big<U, false, 128, 3>(a, p.c, s);
-    }
-    return a.wg ? launch_big<U, true, 256, 2>(a, p.c, s) : launch_big<U, false, 256, 2>(a, p.c, s);
-}
-
-// A call in tiles as p says, and the second kernel where it splits K
-template <int U>
-hipError_t launch_plan(const le::Args<U> &a, Plan p, hipStream_t s)
+// A call in tiles as p says (launch: one of its kernels), and the second kernel where it splits K
+template <int U, class F>
+hipError_t launch_plan(const le::Args<U> &a, Plan p, F launch, hipStream_t s)
 {
     p.c.quads = p.c.split > 1 ? a.N % 4 == 0 : le::quads<U>(a);
-    const hipError_t e = launch_t<U>(a, p, s);
+    const hipError_t e = launch(a, p, s);
     if (e != hipSuccess || p.c.split == 1) return e;
     const bool four = le::quads<U>(a);
     const int wide = four ? 1024 : 256;             // outputs of a workgroup
