@@ -404,7 +404,7 @@ def _rows(name, t, align=1):
     rs, cs = t.stride()
     if cs != 1 and n > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.data_ptr(), rs if T > 1 else (n + align - 1) // align * align
+    return t.data_ptr(), rs if T > 1 else -(-n // align) * align
 
 
 def _workspace(torch, device, nbytes, ws):
@@ -593,17 +593,18 @@ class LinearQ8:
                             _ptr(self.w_gate), _ptr(self.gate_scale), _ptr(self.bias_gate), ACT[self.act])
 
 
-@functools.lru_cache(maxsize=None)
-def _row_dts():
-    """moe_dtype by torch dtype of row operands: those of _dt, and codes."""
-    import torch
-    return {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.int8: MOE_I8}
+_ROW_DT = {}
 
 
 def _row_dt(t) -> int:
-    dt = _row_dts().get(t.dtype)
+    """moe_dtype of a row operand: those of _dt, and codes."""
+    dt = _ROW_DT.get(t.dtype)
     if dt is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
+        import torch
+        _ROW_DT.update({torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32, torch.int8: MOE_I8})
+        dt = _ROW_DT.get(t.dtype)
+        if dt is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
     return dt
 
 
@@ -641,7 +642,7 @@ def linear_q8_forward(linear: LinearQ8, x, *, x_scale=None, residual=None, y=Non
     if linear.bias_gate is not None:
         _want("bias_gate", linear.bias_gate, device, (n,), f32)
     if y is None:
-        y = torch.empty((T, n), dtype=out_dtype or f32, device=device)
+        y = x.new_empty((T, n), dtype=out_dtype or f32)
         yp, ys = y.data_ptr(), n
     else:
         _want("y", y, device, (T, n))
@@ -668,13 +669,13 @@ def quantize_rows(x, *, q=None, scale=None):
         raise ValueError("x must be a GPU tensor")
     T, k = x.shape
     if q is None:
-        q = torch.empty((T, k), dtype=torch.int8, device=device)
+        q = x.new_empty((T, k), dtype=torch.int8)
         qp, qs = q.data_ptr(), k
     else:
         _want("q", q, device, (T, k), torch.int8)
         qp, qs = _rows("q", q)
     if scale is None:
-        scale = torch.empty(T, dtype=torch.float32, device=device)
+        scale = x.new_empty(T, dtype=torch.float32)
     else:
         _want("scale", scale, device, (T,), torch.float32)
     xp, xs = _rows("x", x)
@@ -694,7 +695,7 @@ def dequantize_rows(q, scale, *, y=None, out_dtype=None):
     _want("q", q, device, (T, k), torch.int8)
     _want("scale", scale, device, (T,), torch.float32)
     if y is None:
-        y = torch.empty((T, k), dtype=out_dtype or torch.float32, device=device)
+        y = q.new_empty((T, k), dtype=out_dtype or torch.float32)
         yp, ys = y.data_ptr(), k
     else:
         _want("y", y, device, (T, k))
@@ -723,19 +724,17 @@ class Norm:
         kind = NORM.get(self.kind)
         if kind is None:
             raise ValueError(f"kind must be one of {sorted(NORM)}")
-        dtype, at = None, []
-        for t in (self.w, self.b, self.post_w, self.post_b):
-            if t is None:
-                at.append(None)
-                continue
-            if dtype is None:
-                dtype = t.dtype
-            elif t.dtype != dtype:
-                raise TypeError("the norms' weights and biases must have one dtype")
-            at.append(_ptr(t))
-        return NormDesc(self.d, kind, self.eps, MOE_F32 if dtype is None else _row_dts().get(dtype, -1), at[0], at[1],
-                        int(bool(self.post)), at[2], at[3], int(bool(self.offset)), self.residual_scale,
-                        self.block_scale)
+        wdt, at = None, [None, None, None, None]
+        for i, t in enumerate((self.w, self.b, self.post_w, self.post_b)):
+            if t is not None:
+                if wdt is None:
+                    wdt = t.dtype
+                    dt = _row_dt(t)
+                elif t.dtype != wdt:
+                    raise TypeError("the norms' weights and biases must have one dtype")
+                at[i] = _ptr(t)
+        return NormDesc(self.d, kind, self.eps, MOE_F32 if wdt is None else dt, at[0], at[1], int(bool(self.post)),
+                        at[2], at[3], int(bool(self.offset)), self.residual_scale, self.block_scale)
 
 
 def norm_forward(norm: Norm, residual, block=None, *, gate=None, y=None, out=None, out_dtype=None, out_scale=None):
@@ -752,40 +751,43 @@ def norm_forward(norm: Norm, residual, block=None, *, gate=None, y=None, out=Non
     x = residual if residual is not None else block
     if x is None:
         raise ValueError("norm_forward needs a residual or a block")
-    if x.dim() != 2:
+    shape, device = x.shape, x.device
+    if len(shape) != 2:
         raise ValueError("residual and block must be [T][d]")
-    device = x.device
     if device.type != "cuda":
         raise ValueError("residual and block must be GPU tensors")
-    shape = x.shape
     T, d = shape
     if d != norm.d:
         raise ValueError(f"the rows have {d} columns, the norm d = {norm.d}")
     for t in (norm.w, norm.b, norm.post_w, norm.post_b):
         if t is not None and (t.device != device or t.shape != (d,)):
             _want("a norm's weight or bias", t, device, (d,))
-    like = x if block is None else block
-    rp = bp = gp = yp = op = None
+    rp = bp = gp = yp = op = sp = None
     rs = bs = gs = ys = ns = bdt = odt = 0
+    like = x
+    xdt = _row_dt(x)
     if residual is not None:
         rp, rs = _rows("residual", residual)
     if block is not None:
-        _want("block", block, device, shape)
+        if block.device != device or block.shape != shape:
+            _want("block", block, device, shape)
         bp, bs = _rows("block", block)
         bdt = _row_dt(block)
+        like = block
     if gate is not None:
         if block is None:
             raise ValueError("a gate needs a block")
         _want("gate", gate, device, (d,) if gate.dim() == 1 else shape, block.dtype)
         gp, gs = (_ptr(gate), 0) if gate.dim() == 1 else _rows("gate", gate)
-    if y is None and block is not None:
-        y = torch.empty(shape, dtype=x.dtype, device=device)
-        yp, ys = y.data_ptr(), d
-    elif y is not None and y is not False:
+    if y is None:
+        if block is not None:
+            y = x.new_empty(shape)
+            yp, ys = y.data_ptr(), d
+    elif y is not False:
         _want("y", y, device, shape, x.dtype)
         yp, ys = _rows("y", y)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or like.dtype, device=device)
+        out = like.new_empty(shape) if out_dtype is None or out_dtype is like.dtype else like.new_empty(shape, dtype=out_dtype)
         op, ns = out.data_ptr(), d
     elif out is not False:
         _want("out", out, device, shape)
@@ -793,11 +795,12 @@ def norm_forward(norm: Norm, residual, block=None, *, gate=None, y=None, out=Non
     if op is not None:
         odt = _row_dt(out)
         if odt == MOE_I8 and out_scale is None:
-            out_scale = torch.empty(T, dtype=torch.float32, device=device)
+            out_scale = x.new_empty(T, dtype=torch.float32)
     if out_scale is not None:
         _want("out_scale", out_scale, device, (T,), torch.float32)
-    _call(torch, device, "moe_norm_forward", lib().moe_norm_forward, C.byref(norm.desc()), T, rp, _row_dt(x), rs, bp,
-          bdt, bs, gp, gs, yp, ys, op, odt, ns, None if out_scale is None else _ptr(out_scale))
+        sp = _ptr(out_scale)
+    _call(torch, device, "moe_norm_forward", lib().moe_norm_forward, C.byref(norm.desc()), T, rp, xdt, rs, bp, bdt, bs,
+          gp, gs, yp, ys, op, odt, ns, sp)
     return None if y is False else y, None if out is False else out, out_scale
 
 
