@@ -1101,11 +1101,12 @@ moe_status moe_linear_q8_forward(const moe_linear_q8 *L, const void *x, moe_dtyp
     a.r = residual; a.rs = residual_stride;
     a.y = y; a.ys = y_stride;
     a.part = (float *)w.part;
-    if (!given) {
+    a.xdt = (int)xdt;
+    if (!given && !linear_q8_own_codes(T, k, a.xdt)) {
         QuantizeArgs q{T, k, x, (int)xdt, x_stride, w.q, k, w.scale};
         const hipError_t e = launch_quantize_rows(q, s);
         if (e != hipSuccess) return MOE_ERR_HIP;
-        a.x = (const uint16_t *)w.q; a.xs = k; a.sx = w.scale;
+        a.x = (const uint16_t *)w.q; a.xs = k; a.sx = w.scale; a.xdt = (int)MOE_I8;
     }
     return hip_status(launch_linear_q8(a, s));
 }

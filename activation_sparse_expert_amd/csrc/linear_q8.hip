@@ -36,10 +36,15 @@ hipError_t launch_t(const LinearQ8Args &a, const Plan &p, hipStream_t s)
     return a.wg ? launch_big<U, true, 256, 2>(a, p.c, s) : launch_big<U, false, 256, 2>(a, p.c, s);
 }
 
-// As the 16-bit layer: up to 32 tokens, and small products of a workgroup a compute unit
+// Whether a call streams its weights past the tokens instead: up to 32 tokens, and small
+// products, whose token tiles of 32 and groups of 16 outputs give each compute unit one
+// workgroup (64 x 4096 x 2048 7.2 us against 9.6 in tiles, 64 x 8192 x 2048 10.3 against 12.2, but
+// 40 x 14336 x 2048 17.3 against 14.6) or, over a short k, two (128 x 2048 x 1408 7.2 against
+// 8.5, but 64 x 4096 x 4096 12.3 against 11.9).
 bool q8_streams(int T, int K, int N)
 {
-    return T <= 32 || (K <= 8192 && (long long)((T + 31) / 32) * ((N + 15) / 16) <= kUnits);
+    const long long wgs = (long long)((T + 31) / 32) * ((N + 15) / 16);
+    return T <= 32 || (K <= 5120 && wgs <= kUnits) || (K <= 1280 && wgs <= 2 * kUnits);
 }
 
 }  // namespace
@@ -63,12 +68,23 @@ size_t linear_q8_split_bytes(int T, int K, int N)
     return (np > ng ? np : ng) * (size_t)T * N * 4;
 }
 
+// One token whose numbers and codes leave most of LDS to the weights: a launch less (1 x 4096 x 28672
+// 21.6 us against 23.8 with the codes made first)
+bool linear_q8_own_codes(int T, int K, int xdt)
+{
+    return T == 1 && xdt != 3 && own_raw_bytes(K, xdt) + (K + 127) / 128 * 128 <= 64 * 1024;
+}
+
 hipError_t launch_linear_q8(const LinearQ8Args &given, hipStream_t s)
 {
     LinearQ8Args a = given;
     if (a.T < 1 || a.K < 16 || a.K % 16 != 0 || a.N < 1) return hipErrorInvalidValue;
     a.K /= 2;
     a.xs /= 2;
+    if (a.xdt != 3) {
+        if (!linear_q8_own_codes(a.T, given.K, a.xdt)) return hipErrorInvalidValue;
+        return a.xdt == 2 ? launch_own<2>(a, s) : a.xdt == 1 ? launch_own<1>(a, s) : launch_own<0>(a, s);
+    }
     // (the offsets of a tile's rows have 32 bits)
     if (q8_streams(a.T, a.K, a.N) || a.xs > kTileStride) return launch_stream<st::kI8>(a, s);
     return launch_plan<st::kI8>(a, plan(kTiles, a.T, a.K, a.N, a.wg != nullptr), launch_t, s);

@@ -96,13 +96,13 @@ __device__ __forceinline__ void wait_copies()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// XR: token rows of a block (1, 2, 4 or a multiple of 8)
+// XR: token rows of a block (1, 2, 4 or a multiple of 8), or 0 for one row that is in LDS already
 template <int NM, int XR, int U = kF16>
 struct Ring {
     static constexpr int kTok = (XR + 7) / 8;           // copy instructions of tokens
     static constexpr int kCopies = 2 * NM + kTok;       // instructions per block
     static constexpr int kBlock = 2048 * NM + 128 * XR; // bytes
-    static constexpr int kFrag = (XR + 15) / 16;        // groups of 16 tokens
+    static constexpr int kFrag = XR ? (XR + 15) / 16 : 1;      // groups of 16 tokens
     typedef typename Sum<U>::x4 Acc[NM][kFrag];
     typedef const uint16_t *Src[kCopies];
 };
@@ -117,11 +117,18 @@ __device__ __forceinline__ int copy_k(int lane) { return 8 * ((lane & 7) ^ (lane
 //   src[i]: this lane's source of copy i at the first block (copy_row, copy_k):
 //           2 NM of weights (rows 8 i ..), then those of the XR token rows
 //   ring:   D blocks of LDS of this wave (wave-uniform)
+//   row:    XR 0: the token's part of the first block in LDS, 128 bytes a block
+//   ready:  called once the first blocks are on their way (all D - 1 of them, or fewer): what
+//           the row needs before it is read
 // Columns of D past the XR rows repeat some of them; rows and tokens that do not
 // exist may be given as copies of others: their part of D means nothing.
-template <int U, int NM, int XR, int D>
+struct Nothing {
+    __device__ __forceinline__ void operator()(bool) const {}
+};
+template <int U, int NM, int XR, int D, class F = Nothing>
 __device__ __forceinline__ void stream(typename Ring<NM, XR, U>::Acc &acc, unsigned char *ring,
-                                       typename Ring<NM, XR, U>::Src &src, int nb, int kl, int lane)
+                                       typename Ring<NM, XR, U>::Src &src, int nb, int kl, int lane,
+                                       const unsigned char *row = nullptr, F ready = F())
 {
     using R = Ring<NM, XR, U>;
     static_assert(XR == 1 || XR == 2 || XR == 4 || XR % 8 == 0, "token rows");
@@ -151,6 +158,10 @@ __device__ __forceinline__ void stream(typename Ring<NM, XR, U>::Acc &acc, unsig
             for (int m = 0; m < NM; ++m) w[m] = *(const uint4 *)(d + 2048 * m + at);
 #pragma unroll
             for (int j = 0; j < R::kFrag; ++j) {
+                if constexpr (XR == 0) {
+                    x[j] = *(const uint4 *)(row + 16 * c);
+                    continue;
+                }
                 int xt = at;
                 if (XR == 1) xt = 16 * c;
                 else if (XR < 8) xt = (li & (XR - 1)) * 128 + 16 * (c ^ (li & (XR - 1)));
@@ -162,12 +173,14 @@ __device__ __forceinline__ void stream(typename Ring<NM, XR, U>::Acc &acc, unsig
 #pragma unroll
                 for (int j = 0; j < R::kFrag; ++j) acc[m][j] = mma16<U>(w[m], x[j], acc[m][j]);
         }
+        if (XR == 0) row += 128;
         // the block's reads are done before a copy may fill its place
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     };
 #pragma unroll
     for (int i = 0; i < D - 1; ++i)
         if (i < nb) issue();
+    ready(nb >= D - 1);
     int b = 0;
     for (; b + D - 1 < nb; ++b) {
         wait_copies<R::kCopies * (D - 2)>();            // block b has landed

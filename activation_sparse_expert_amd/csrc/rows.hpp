@@ -61,10 +61,12 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t s);
 // The linear layer on codes: products of the base's x and w (codes; strides and K in
 // elements, that is bytes) times sx[t] sw[j], then as the linear layer.
 struct LinearQ8Args : LinearArgs {
-    const float *sx;                    // [T]
+    int xdt;                            // type of x: 3 codes, else one token that the kernel makes codes of
+    const float *sx;                    // [T] (codes)
     const float *sw, *sg;               // [N] scales of w and wg
 };
 hipError_t launch_linear_q8(const LinearQ8Args &a, hipStream_t s);
+bool linear_q8_own_codes(int T, int K, int xdt);        // whether it makes codes of such tokens
 // The parts of K of a call (0: streamed) and its tile
 int linear_q8_parts(int T, int K, int N, bool gated, int *bm, int *bn);
 size_t linear_q8_split_bytes(int T, int K, int N);      // partial products, enough for the plain and the gated call

@@ -138,6 +138,32 @@ def test_infinities_and_nan_stay_in_their_row_and_column(T):
     assert not bool(torch.isfinite(y[3:, n - 1]).any())
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("k", [16, 128, 1040, 10240, 14336, 20480, 32768])
+def test_one_token_of_any_length(k, kind):
+    """Codes made by the product's own workgroups or, of long tokens, before it: the same outputs; rows
+    of zeros, with a NaN, an infinity, and of the smallest and largest numbers."""
+    g = gen(k)
+    fi = torch.finfo(DT[kind])
+    for n, gated in ((17, False), (300, True), (9000, False)):
+        lin = layer(g, n, k, gated, True, "silu")
+        base = normal(g, (1, k), DT[kind])
+        for change in (None, 0.0, float("nan"), float("inf"), fi.max, fi.smallest_normal * fi.eps):
+            x = base.clone()
+            if change == 0.0 or (change is not None and change == change and change < 1):
+                x.zero_()
+            if change is not None:
+                x[0, k - 1] = change
+            q, s = codes64(x)
+            y = moe.linear_q8_forward(lin, x)
+            # (a row with an infinity or a NaN has the scale NaN)
+            assert torch.equal(y.isnan(), ~s.isfinite()[:, None].expand_as(y)), f"{n} {change}"
+            given = moe.linear_q8_forward(lin, *moe.quantize_rows(x)[:1], x_scale=moe.quantize_rows(x)[1])
+            assert bool(((y == given) | (y.isnan() & given.isnan())).all()), f"{n} {change}"
+            if change is None:
+                check(y, *linear_q8_64(q, s, lin), f"{n}")
+
+
 @pytest.mark.parametrize("T", [1, 20, 48, 300])
 def test_graph_replays_follow_their_inputs(T):
     """Two graphs on one workspace, replayed in turn with eager work between."""

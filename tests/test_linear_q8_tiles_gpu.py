@@ -43,7 +43,7 @@ def test_every_tile_against_64_bits(T, k, n, tile, gated, split):
 
 
 # (T, k, n, gated) with n a multiple of 4, so that outputs may go by fours
-QUADS = [(36, 400, 2152, True), (276, 448, 11212, False), (67, 2736, 1364, True), (68, 4816, 4224, False),
+QUADS = [(130, 400, 2152, True), (276, 448, 11212, False), (67, 2736, 1364, True), (68, 4816, 4224, False),
          (70, 15984, 4324, False), (2000, 1136, 2048, False)]
 
 
