@@ -39,7 +39,7 @@ struct OwnCodes {
         __syncthreads();
         uint32_t most = 0;
         for (int i = 8 * threadIdx.x; i < k; i += 8 * blockDim.x)
-            most = rio::umax(most, rio::most<XDT == 2>(rio::load<XDT == 2, true>(raw, XDT, i, 8), XDT));
+            most = rio::umax(most, rio::most<XDT == 2>(rio::load<XDT == 2, true>(raw, XDT, i, 8, 0), XDT));
         most = rio::seg_max<64>(most);
         if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = most;
         __syncthreads();
@@ -48,10 +48,10 @@ struct OwnCodes {
         for (int i = 8 * threadIdx.x; i < pad; i += 8 * blockDim.x) {
             float v[8];
             uint32_t q[8];
-            rio::floats<XDT == 2>(rio::load<XDT == 2, true>(raw, XDT, i < k ? i : 0, 8), XDT, v);
+            rio::floats<XDT == 2>(rio::load<XDT == 2, true>(raw, XDT, i < k ? i : 0, 8, 0), XDT, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[j] = XDT == 2 ? codes::code64(v[j], row) : codes::code(v[j], row);
-            rio::store_codes<true>((int8_t *)codes, i, 8, q, row.ok && i < k);
+            rio::store_codes<true>((int8_t *)codes, i, 8, 0, q, row.ok && i < k);
         }
         __syncthreads();
     }

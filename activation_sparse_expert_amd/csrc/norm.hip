@@ -55,7 +55,7 @@ __device__ __forceinline__ void norm_row(float (&v)[C][8], const int (&n)[C], ri
         }
         if (b) {
             float x[8];
-            rio::floats<WIDE>(rio::load<WIDE, FULL>(b, a.wdt, 8 * (team.lane() + c * team.lanes()), n[c]), a.wdt, x);
+            rio::floats<WIDE>(rio::load<WIDE, FULL>(b, a.wdt, 8 * (team.lane() + c * team.lanes()), n[c], a.d & 7), a.wdt, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[c][j] += x[j];
         }
@@ -79,9 +79,9 @@ norm_kernel(NormArgs a)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             n[c] = t < a.T ? a.d - at[c] : 0;
-            if (!BARE) orw[c] = rio::load<WIDE, FULL>(rio::at(a.o, a.odt, t * a.os), a.odt, at[c], n[c]);
-            if (a.r) rr[c] = rio::load<WIDE, FULL>(rio::at(a.r, a.rdt, t * a.rs), a.rdt, at[c], n[c]);
-            if (!BARE && a.g && (first || a.gs)) gr[c] = rio::load<WIDE, FULL>(rio::at(a.g, a.odt, t * a.gs), a.odt, at[c], n[c]);
+            if (!BARE) orw[c] = rio::load<WIDE, FULL>(rio::at(a.o, a.odt, t * a.os), a.odt, at[c], n[c], a.d & 7);
+            if (a.r) rr[c] = rio::load<WIDE, FULL>(rio::at(a.r, a.rdt, t * a.rs), a.rdt, at[c], n[c], a.d & 7);
+            if (!BARE && a.g && (first || a.gs)) gr[c] = rio::load<WIDE, FULL>(rio::at(a.g, a.odt, t * a.gs), a.odt, at[c], n[c], a.d & 7);
         }
     };
     long long base = blockIdx.x;
@@ -90,8 +90,8 @@ norm_kernel(NormArgs a)
     load_row(base * G + team.row(), true);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        if (!BARE && a.pw) pwr[c] = rio::load<WIDE, FULL>(a.pw, a.wdt, at[c], a.d - at[c]);
-        if (a.w) wr[c] = rio::load<WIDE, FULL>(a.w, a.wdt, at[c], a.d - at[c]);
+        if (!BARE && a.pw) pwr[c] = rio::load<WIDE, FULL>(a.pw, a.wdt, at[c], a.d - at[c], a.d & 7);
+        if (a.w) wr[c] = rio::load<WIDE, FULL>(a.w, a.wdt, at[c], a.d - at[c], a.d & 7);
     }
     for (; base * G < a.T; base += gridDim.x) {
         const long long t = base * G + team.row();
@@ -133,13 +133,13 @@ norm_kernel(NormArgs a)
         if ((base + gridDim.x) * G < a.T) load_row(t + (long long)gridDim.x * G, false);
         if (a.y) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) rio::store<FULL>(rio::at(a.y, a.rdt, t * a.ys), a.rdt, at[c], m[c], v[c]);
+            for (int c = 0; c < C; ++c) rio::store<FULL>(rio::at(a.y, a.rdt, t * a.ys), a.rdt, at[c], m[c], a.d & 7, v[c]);
         }
         if (!a.out) continue;
         norm_row<L, C, WIDE, FULL, BARE>(v, m, team, a, a.w, wr, a.b);
         if (a.ndt != 3) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) rio::store<FULL>(rio::at(a.out, a.ndt, t * a.ns), a.ndt, at[c], m[c], v[c]);
+            for (int c = 0; c < C; ++c) rio::store<FULL>(rio::at(a.out, a.ndt, t * a.ns), a.ndt, at[c], m[c], a.d & 7, v[c]);
             continue;
         }
         uint32_t most = 0;
@@ -153,7 +153,7 @@ norm_kernel(NormArgs a)
             uint32_t q[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[j] = codes::code(v[c][j], r);
-            rio::store_codes<FULL>((int8_t *)a.out + t * a.ns, at[c], m[c], q, r.ok);
+            rio::store_codes<FULL>((int8_t *)a.out + t * a.ns, at[c], m[c], a.d & 7, q, r.ok);
         }
         if (team.lane() == 0 && live) a.out_scale[t] = r.scale;
     }

@@ -23,7 +23,7 @@ quantize_kernel(QuantizeArgs a)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             n[c] = t < a.T ? a.k - at[c] : 0;
-            raw[c] = rio::load<XDT == 2>(rio::at(a.x, XDT, t * a.xs), XDT, at[c], n[c]);
+            raw[c] = rio::load<XDT == 2>(rio::at(a.x, XDT, t * a.xs), XDT, at[c], n[c], a.k & 7);
         }
     };
 #pragma unroll
@@ -49,7 +49,7 @@ quantize_kernel(QuantizeArgs a)
             uint32_t q[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[j] = XDT == 2 ? codes::code64(v[c][j], r) : codes::code(v[c][j], r);
-            rio::store_codes(a.q + t * a.qs, at[c], m[c], q, r.ok);
+            rio::store_codes(a.q + t * a.qs, at[c], m[c], a.k & 7, q, r.ok);
         }
         if (team.lane() == 0 && t < a.T) a.scale[t] = r.scale;
     }
@@ -67,16 +67,16 @@ quantize_long_kernel(QuantizeArgs a)
         int8_t *qr = a.q + t * a.qs;
         uint32_t most = 0;
         for (int i = 8 * threadIdx.x; i < a.k; i += 8 * 1024) {
-            most = rio::umax(most, rio::most<XDT == 2>(rio::load<XDT == 2>(x, XDT, i, a.k - i), XDT));
+            most = rio::umax(most, rio::most<XDT == 2>(rio::load<XDT == 2>(x, XDT, i, a.k - i, a.k & 7), XDT));
         }
         const codes::Row r = codes::row(team.max(most));
         for (int i = 8 * threadIdx.x; i < a.k; i += 8 * 1024) {
             float v[8];
             uint32_t q[8];
-            rio::floats<XDT == 2>(rio::load<XDT == 2>(x, XDT, i, a.k - i), XDT, v);
+            rio::floats<XDT == 2>(rio::load<XDT == 2>(x, XDT, i, a.k - i, a.k & 7), XDT, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) q[j] = XDT == 2 ? codes::code64(v[j], r) : codes::code(v[j], r);
-            rio::store_codes(qr, i, a.k - i, q, r.ok);
+            rio::store_codes(qr, i, a.k - i, a.k & 7, q, r.ok);
         }
         if (threadIdx.x == 0) a.scale[t] = r.scale;
     }
@@ -94,18 +94,22 @@ dequantize_kernel(DequantizeArgs a, int parts)
         const float s = a.scale[t];
         for (int i = first; i < a.k; i += 8 * L * parts) {
             const int8_t *p = a.q + t * a.qs + i;
-            int8_t q[8] = {};
+            uint2 q = make_uint2(0, 0);
             if (a.k - i >= 8) {
-                __builtin_memcpy(q, p, 8);
+                q = rio::read_any<uint2>(p);
             } else {
-#pragma unroll
-                for (int j = 0; j < 7; ++j)
-                    if (j < a.k - i) q[j] = p[j];
+                const int tail = a.k & 7;
+                uint32_t rest = 0;
+                if (tail & 4) q.x = rio::read_any<uint32_t>(p);
+                if (tail & 2) rest = rio::read_any<uint16_t>(p + (tail & 4));
+                if (tail & 1) rest |= (uint32_t)(uint8_t)p[tail & 6] << (tail & 2 ? 16 : 0);
+                if (tail & 4) q.y = rest;
+                else q.x = rest;
             }
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = (float)q[j] * s;
-            rio::store(rio::at(a.y, a.ydt, t * a.ys), a.ydt, i, a.k - i, v);
+            for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)((j < 4 ? q.x : q.y) >> 8 * (j & 3)) * s;
+            rio::store(rio::at(a.y, a.ydt, t * a.ys), a.ydt, i, a.k - i, a.k & 7, v);
         }
     }
 }

@@ -31,10 +31,21 @@ __device__ __forceinline__ uint4 load16(const void *p)
     return v;
 }
 
-// Elements i .. i + n - 1 (n up to 8, or 8 and more; none if n <= 0), zeros past them.  FULL: no
-// other n than these between 0 and 8.
+template <class T>
+__device__ __forceinline__ T read_any(const void *p)
+{
+    T v;
+    __builtin_memcpy(&v, p, sizeof(T));
+    return v;
+}
+template <class T>
+__device__ __forceinline__ void write_any(void *p, T v) { __builtin_memcpy(p, &v, sizeof(T)); }
+
+// Elements i .. i + 7 of a row, or where n < 8 the row's last n, zeros past them; none if n <= 0.
+// `tail` is what n is wherever 0 < n < 8, the same for all lanes: those elements go by
+// four, two and one.  FULL: there is no such n.
 template <bool WIDE, bool FULL = false>
-__device__ __forceinline__ Raw<WIDE> load(const void *p, int dt, uint32_t i, int n)
+__device__ __forceinline__ Raw<WIDE> load(const void *p, int dt, uint32_t i, int n, int tail)
 {
     Raw<WIDE> r{};
     if (n >= 8) {
@@ -45,18 +56,30 @@ __device__ __forceinline__ Raw<WIDE> load(const void *p, int dt, uint32_t i, int
             r.b = load16((const float *)p + i + 4);
         }
     } else if (!FULL && n > 0) {
-        uint32_t v[8] = {};
         if (!WIDE || dt != 2) {
-#pragma unroll
-            for (int j = 0; j < 7; ++j)
-                if (j < n) v[j] = ((const uint16_t *)p)[i + j];
-            r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6]);
+            const uint16_t *q = (const uint16_t *)p + i;
+            uint2 four = make_uint2(0, 0);
+            uint32_t two = 0, one = 0;
+            if (tail & 4) four = read_any<uint2>(q);
+            if (tail & 2) two = read_any<uint32_t>(q + (tail & 4));
+            if (tail & 1) one = q[tail & 6];
+            if (tail & 4) r.a = tail & 2 ? make_uint4(four.x, four.y, two, one) : make_uint4(four.x, four.y, one, 0);
+            else r.a = tail & 2 ? make_uint4(two, one, 0, 0) : make_uint4(one, 0, 0, 0);
         } else if constexpr (WIDE) {
-#pragma unroll
-            for (int j = 0; j < 7; ++j)
-                if (j < n) v[j] = ((const uint32_t *)p)[i + j];
-            r.a = make_uint4(v[0], v[1], v[2], v[3]);
-            r.b = make_uint4(v[4], v[5], v[6], 0);
+            const uint32_t *q = (const uint32_t *)p + i;
+            uint4 four = make_uint4(0, 0, 0, 0);
+            uint2 two = make_uint2(0, 0);
+            uint32_t one = 0;
+            if (tail & 4) four = read_any<uint4>(q);
+            if (tail & 2) two = read_any<uint2>(q + (tail & 4));
+            if (tail & 1) one = q[tail & 6];
+            const uint4 rest = tail & 2 ? make_uint4(two.x, two.y, one, 0) : make_uint4(one, 0, 0, 0);
+            if (tail & 4) {
+                r.a = four;
+                r.b = rest;
+            } else {
+                r.a = rest;
+            }
         }
     }
     return r;
@@ -101,38 +124,53 @@ __device__ __forceinline__ uint32_t pair16(float a, float b)
     return st::to16<BF16>(a) | (uint32_t)st::to16<BF16>(b) << 16;
 }
 
+// As load
 template <bool FULL = false>
-__device__ __forceinline__ void store(void *p, int dt, uint32_t i, int n, const float (&v)[8])
+__device__ __forceinline__ void store(void *p, int dt, uint32_t i, int n, int tail, const float (&v)[8])
 {
-    if (n >= 8) {
-        if (dt == 2) {
-            __builtin_memcpy((float *)p + i, v, 32);
-        } else {
-            const uint4 w = dt == 1 ? make_uint4(pair16<true>(v[0], v[1]), pair16<true>(v[2], v[3]),
-                                                 pair16<true>(v[4], v[5]), pair16<true>(v[6], v[7]))
-                                    : make_uint4(pair16<false>(v[0], v[1]), pair16<false>(v[2], v[3]),
-                                                 pair16<false>(v[4], v[5]), pair16<false>(v[6], v[7]));
-            __builtin_memcpy((uint16_t *)p + i, &w, 16);
+    if (dt == 2) {
+        float *q = (float *)p + i;
+        if (n >= 8) {
+            __builtin_memcpy(q, v, 32);
+        } else if (!FULL && n > 0) {
+            // (named, so that the choice is between registers and not between places of an array)
+            const float v0 = v[0], v1 = v[1], v2 = v[2], v4 = v[4], v5 = v[5], v6 = v[6];
+            const bool f = tail & 4, t = tail & 2;
+            const float a = f ? v4 : v0, b = f ? v5 : v1, c = f ? v6 : v2;
+            if (f) write_any(q, make_float4(v0, v1, v2, v[3]));
+            if (t) write_any(q + (tail & 4), make_float2(a, b));
+            if (tail & 1) q[tail & 6] = t ? c : a;
         }
-    } else if (!FULL) {
-#pragma unroll
-        for (int j = 0; j < 7; ++j)
-            if (j < n) st::store_el(p, dt, i + j, v[j]);
+        return;
+    }
+    uint4 w;
+    if (dt == 1) w = make_uint4(pair16<true>(v[0], v[1]), pair16<true>(v[2], v[3]), pair16<true>(v[4], v[5]), pair16<true>(v[6], v[7]));
+    else w = make_uint4(pair16<false>(v[0], v[1]), pair16<false>(v[2], v[3]), pair16<false>(v[4], v[5]), pair16<false>(v[6], v[7]));
+    uint16_t *q = (uint16_t *)p + i;
+    if (n >= 8) {
+        write_any(q, w);
+    } else if (!FULL && n > 0) {
+        const bool f = tail & 4, t = tail & 2;
+        if (f) write_any(q, make_uint2(w.x, w.y));
+        if (t) write_any(q + (tail & 4), f ? w.z : w.x);
+        if (tail & 1) q[tail & 6] = (uint16_t)(f ? (t ? w.w : w.z) : t ? w.y : w.x);
     }
 }
 
 // Codes from the bits that codes::code gives, zeros unless ok
 template <bool FULL = false>
-__device__ __forceinline__ void store_codes(int8_t *p, uint32_t i, int n, const uint32_t (&q)[8], bool ok)
+__device__ __forceinline__ void store_codes(int8_t *p, uint32_t i, int n, int tail, const uint32_t (&q)[8], bool ok)
 {
     uint2 w = make_uint2(codes::pack4(q[0], q[1], q[2], q[3]), codes::pack4(q[4], q[5], q[6], q[7]));
     if (!ok) w = make_uint2(0, 0);
+    p += i;
     if (n >= 8) {
-        __builtin_memcpy(p + i, &w, 8);
-    } else if (!FULL) {
-#pragma unroll
-        for (int j = 0; j < 7; ++j)
-            if (j < n) p[i + j] = (int8_t)((j < 4 ? w.x : w.y) >> 8 * (j & 3));
+        write_any(p, w);
+    } else if (!FULL && n > 0) {
+        const uint32_t r = tail & 4 ? w.y : w.x;
+        if (tail & 4) write_any(p, w.x);
+        if (tail & 2) write_any(p + (tail & 4), (uint16_t)r);
+        if (tail & 1) p[tail & 6] = (int8_t)(tail & 2 ? r >> 16 : r);
     }
 }
 
