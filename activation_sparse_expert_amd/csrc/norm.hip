@@ -101,7 +101,7 @@ norm_kernel(NormArgs a)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             m[c] = n[c];
-            if constexpr (C > 1) {
+            if constexpr (C > 1 || (WIDE && !FULL)) {
                 rio::stay_packed<WIDE>(wr[c]);
                 if (!BARE) rio::stay_packed<WIDE>(pwr[c]);
                 if (!BARE) rio::stay_packed<WIDE>(gr[c]);
