@@ -205,16 +205,11 @@ __device__ __forceinline__ void add_store4(const LinearArgs &p, const uint4 &r, 
     }
 }
 
-// Outputs n .. n + 3 (n a multiple of 4, all below N) of token t
+// Outputs n .. n + 3 (n a multiple of 4, all below N) of token t, with scale sx and residual r
 template <int U>
-__device__ __forceinline__ void finish_bits4(const Args<U> &p, int t, int n, float (&v)[4], float (&g)[4])
+__device__ __forceinline__ void finish_cols4(const Args<U> &p, const Cols &c, float sx, const uint4 &r, int t, int n,
+                                             float (&v)[4], float (&g)[4])
 {
-    Cols c;
-    load_cols<U>(p, c, n, true);
-    float sx = 0.f;
-    if constexpr (U == st::kI8) sx = p.sx[t];
-    uint4 r{};
-    if (p.r) r = load_residual(p, (size_t)t * p.rs + n, 4, true);
     apply_cols<U, -1>(p, c, sx, v, g);
     const size_t at = (size_t)t * p.ys + n;
     auto store = [&](auto res) {

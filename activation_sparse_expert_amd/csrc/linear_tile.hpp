@@ -207,24 +207,26 @@ struct StoreTile {
     __device__ __forceinline__ void parts(int t0)
     {
         const size_t plane = (size_t)a.T * a.N;
+        float *p = a.part + (size_t)ks * (GATED ? 2 : 1) * plane + (size_t)(t0 + first) * a.N + n;
+        const int end = m <= 0 ? 0 : min(a.T - t0, 32);
+        if (quads) {
+#pragma unroll 4
+            for (int t = first; t < end; t += kStep, p += (size_t)kStep * a.N) {
+                *(float4 *)p = *(const float4 *)&lds[t * LD + col];
+                if (GATED) *(float4 *)(p + plane) = *(const float4 *)&lds[t * LD + col + 32 * HN];
+            }
+            return;
+        }
 #pragma unroll 1
-        for (int t = first; t < 32; t += kStep) {
-            const int tok = t0 + t;
-            if (m <= 0 || tok >= a.T) break;
+        for (int t = first; t < end; t += kStep, p += (size_t)kStep * a.N) {
             float v[4], g[4];
             sums(t, v, g);
-            float *p = a.part + (size_t)ks * (GATED ? 2 : 1) * plane + (size_t)tok * a.N + n;
-            if (quads) {
-                *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]);
-                if (GATED) *(float4 *)(p + plane) = make_float4(g[0], g[1], g[2], g[3]);
-            } else {
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (x < m) {
-                        p[x] = v[x];
-                        if (GATED) p[plane + x] = g[x];
-                    }
-            }
+            for (int x = 0; x < 4; ++x)
+                if (x < m) {
+                    p[x] = v[x];
+                    if (GATED) p[plane + x] = g[x];
+                }
         }
     }
 };
@@ -524,8 +526,15 @@ linear_join_kernel(le::Args<U> a, int split)
     const int n = Q * (blockIdx.x * 256 + threadIdx.x), nm = a.wg ? 2 : 1;
     const size_t plane = (size_t)a.T * a.N;
     if (n >= a.N) return;
+    le::Cols cols;
+    if constexpr (Q == 4) le::load_cols<U>(a, cols, n, true);
     for (int t = blockIdx.y; t < a.T; t += gridDim.y) {
-        float v[2][Q] = {};
+        float v[2][Q] = {}, sx = 0.f;
+        uint4 r{};
+        if constexpr (Q == 4) {
+            if constexpr (U == st::kI8) sx = a.sx[t];
+            if (a.r) r = le::load_residual(a, (size_t)t * a.rs + n, 4, true);
+        }
         for (int m = 0; m < nm; ++m) {
             const float *p = a.part + m * plane + (size_t)t * a.N + n;
             float q[kMaxSplit][Q];
@@ -542,7 +551,7 @@ linear_join_kernel(le::Args<U> a, int split)
 #pragma unroll
                     for (int x = 0; x < Q; ++x) v[m][x] = le::add_bits<U>(v[m][x], q[s][x]);
         }
-        if constexpr (Q == 4) le::finish_bits4<U>(a, t, n, v[0], v[1]);
+        if constexpr (Q == 4) le::finish_cols4<U>(a, cols, sx, r, t, n, v[0], v[1]);
         else le::finish_bits<U>(a, t, n, v[0][0], v[1][0]);
     }
 }
