@@ -15,7 +15,7 @@
 // before the epilogue.  plan() chooses by what each was measured to cost.
 // 4096 x 4096 x (2 x 14336), gated: 780-850 us, 1130-1230 TFLOP/s (MFMA busy 62%
 // of the cycles at the 1.75 GHz that the power limit leaves).  300 x 4096 x 4096:
-// 22 us in 128 x 256 tiles and 4 parts of K, and 5.6 us for their sum: 16 blocks of
+// 22.4 us in 128 x 256 tiles and 4 parts of K, and 5.7 us for their sum: 16 blocks of
 // 0.88 us, of which the MFMAs are 0.43, and the start and end of the tile.
 #pragma once
 #include "linear_epilogue.hpp"
@@ -518,7 +518,7 @@ constexpr int kMaxSplit = 8;
 // Sum of the split's products, in order, and the epilogue: a thread takes four outputs
 // of a token where they can be read and written together (Q 4), else one, and
 // loads all their products before it uses the first (4096 outputs of 300 tokens
-// in four parts: 5.6 us, against 8.4 by single outputs and loads).
+// in four parts: 5.7 us, against 8.4 by single outputs and loads).
 template <int U, int Q>
 __global__ void __launch_bounds__(256)
 linear_join_kernel(le::Args<U> a, int split)

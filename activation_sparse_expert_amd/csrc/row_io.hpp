@@ -1,6 +1,6 @@
 // Eight neighbouring elements of a row at a time, of any type and at any address: whole
 // groups are loads and stores of 16 bytes (8 for codes), which gfx950 takes at the
-// alignment of an element; a row's last group goes by elements.
+// alignment of an element; a row's last elements go by four, two and one.
 #pragma once
 #include "codes.hpp"
 #include "mfma_stream.hpp"
