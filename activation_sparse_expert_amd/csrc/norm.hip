@@ -1,7 +1,7 @@
 // Norms between two blocks: y = rs r + bs g (.) Npost(o), out = Npre(y).  Bound by HBM: a row
 // is held in registers by the lanes of part of a wave, or by a workgroup, so that each
 // operand is read and written once, and mean and squares are two passes over registers.
-// 131072 x 128, bf16: 14 us, 4.8 TB/s; 4096 x 6144 between two norms to codes: 48 us, 3.7 TB/s
+// 131072 x 128, bf16: 14 us, 4.8 TB/s; 4096 x 6144 between two norms to codes: 46 us, 3.8 TB/s
 // (three reductions over a workgroup a row, the next row's loads under way); one row 3.2 us, the
 // launch.
 #include "row_io.hpp"
@@ -78,11 +78,16 @@ norm_kernel(NormArgs a)
     constexpr int G = L ? 256 / (L ? L : 1) : 1;
     int n[C], at[C];
     rio::Raw<WIDE> rr[C], orw[C], gr[C], wr[C], pwr[C];
-    auto load_row = [&](long long t, bool first) {
+    auto load_block = [&](long long t) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             n[c] = t < a.T ? a.d - at[c] : 0;
             if (!BARE) orw[c] = rio::load<WIDE, FULL>(rio::at(a.o, a.odt, t * a.os), a.odt, at[c], n[c], a.d & 7);
+        }
+    };
+    auto load_rest = [&](long long t, bool first) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
             if (a.r) rr[c] = rio::load<WIDE, FULL>(rio::at(a.r, a.rdt, t * a.rs), a.rdt, at[c], n[c], a.d & 7);
             if (!BARE && a.g && (first || a.gs)) gr[c] = rio::load<WIDE, FULL>(rio::at(a.g, a.odt, t * a.gs), a.odt, at[c], n[c], a.d & 7);
         }
@@ -90,7 +95,8 @@ norm_kernel(NormArgs a)
     long long base = blockIdx.x;
 #pragma unroll
     for (int c = 0; c < C; ++c) at[c] = 8 * (team.lane() + c * team.lanes());
-    load_row(base * G + team.row(), true);
+    load_block(base * G + team.row());
+    load_rest(base * G + team.row(), true);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         if (!BARE && a.pw) pwr[c] = rio::load<WIDE, FULL>(a.pw, a.wdt, at[c], a.d - at[c], a.d & 7);
@@ -113,6 +119,15 @@ norm_kernel(NormArgs a)
         if (!BARE) {
 #pragma unroll
             for (int c = 0; c < C; ++c) rio::floats<WIDE>(orw[c], a.odt, v[c]);
+        }
+        // The next row of these lanes is on its way while this one is finished, its block from before
+        // the block's norm where that hides more than the registers cost: 2048 x 8192 between norms to
+        // codes 29.6 us against 32.6, but in one group of 16-bit numbers 8192 x 2048 31.4 against 29.3.
+        constexpr bool kEarly = C > 1 || WIDE;
+        const long long next = t + (long long)gridDim.x * G;
+        const bool more = (base + gridDim.x) * G < a.T;
+        if (kEarly && more) load_block(next);
+        if (!BARE) {
             if (a.post) norm_row<L, C, WIDE, FULL, BARE>(v, m, team, a, a.pw, pwr, a.pb);
         }
 #pragma unroll
@@ -132,8 +147,8 @@ norm_kernel(NormArgs a)
                 for (int j = 0; j < 8; ++j) v[c][j] += a.rscale * r[j];
             }
         }
-        // the next row of these lanes is on its way while this one is finished
-        if ((base + gridDim.x) * G < a.T) load_row(t + (long long)gridDim.x * G, false);
+        if (!kEarly && more) load_block(next);
+        if (more) load_rest(next, false);
         if (a.y) {
 #pragma unroll
             for (int c = 0; c < C; ++c) rio::store<FULL>(rio::at(a.y, a.rdt, t * a.ys), a.rdt, at[c], m[c], a.d & 7, v[c]);
@@ -165,7 +180,7 @@ norm_kernel(NormArgs a)
 template <bool WIDE, bool FULL, bool BARE>
 hipError_t launch(const NormArgs &a, hipStream_t s)
 {
-    // two groups a lane: 4096 x 6144 between norms to 8 bits 47 us against 52, 2048 x 8192 32 against 35;
+    // two groups a lane: 4096 x 6144 between norms to 8 bits 46 us against 52, 2048 x 8192 30 against 35;
     // 4096 x 4096 28 against 28; with 32-bit operands, whose registers then spill, 71 against 42
     const rio::Shape h = rio::shape(a.d, WIDE || a.T <= 512 ? rio::kGroups : FULL ? 512 : 256);
     const dim3 g(rio::grid(h, a.T, h.groups == 2 ? 1024 : 2048)), b(h.threads);
