@@ -7,14 +7,16 @@
 #include "row_io.hpp"
 #include "rows.hpp"
 
-#include <algorithm>
+#include <cfloat>
 
 namespace moeffn {
 
 namespace {
 
-// The norm of a row in place, n[c] of whose elements each group of this lane holds.  Where the
-// squares pass fp32 everything is taken of values 2^-80 as large, beside which eps is nothing.
+// The norm of a row in place, n[c] of whose elements each group of this lane holds.  Where a sum
+// or the squares pass fp32 everything is taken of values 2^-80 as large, eps of 2^-160 of itself
+// (0 below 2^11: beside squares that pass fp32 that is nothing, and of equal values,
+// whose sum alone does, v - m is 0 and what is under the root need only not be).
 template <int L, int C, bool WIDE, bool FULL, bool BARE>
 __device__ __forceinline__ void norm_row(float (&v)[C][8], const int (&n)[C], rio::Team<L> &team, const NormArgs &a,
                                          const void *w, const rio::Raw<WIDE> (&wr)[C], const void *b)
@@ -45,7 +47,8 @@ __device__ __forceinline__ void norm_row(float (&v)[C][8], const int (&n)[C], ri
         k = ss < INFINITY ? 1.f : 0x1p-80f;
         stats();
     }
-    const float f = __builtin_amdgcn_rsqf(ss * inv + (k == 1.f ? a.eps : 0.f));
+    const float var = ss * inv + a.eps * k * k;
+    const float f = __builtin_amdgcn_rsqf(var < FLT_MIN ? FLT_MIN : var);      // (a NaN stays one)
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
