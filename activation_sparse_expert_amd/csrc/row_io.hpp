@@ -85,12 +85,20 @@ __device__ __forceinline__ Raw<WIDE> load(const void *p, int dt, uint32_t i, int
     return r;
 }
 
-// Keeps the compiler from unpacking r before a loop, which would hold it in twice the registers
+// Keeps the compiler from unpacking r before a loop, which would hold it in twice the registers.  (Four
+// registers at once: by members, some are copied as soon as they are loaded, and the load waited for.)
 template <bool WIDE>
 __device__ __forceinline__ void stay_packed(Raw<WIDE> &r)
 {
-    asm volatile("" : "+v"(r.a.x), "+v"(r.a.y), "+v"(r.a.z), "+v"(r.a.w));
-    if constexpr (WIDE) asm volatile("" : "+v"(r.b.x), "+v"(r.b.y), "+v"(r.b.z), "+v"(r.b.w));
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 a = __builtin_bit_cast(u32x4, r.a);
+    asm volatile("" : "+v"(a));
+    r.a = __builtin_bit_cast(uint4, a);
+    if constexpr (WIDE) {
+        u32x4 b = __builtin_bit_cast(u32x4, r.b);
+        asm volatile("" : "+v"(b));
+        r.b = __builtin_bit_cast(uint4, b);
+    }
 }
 
 template <bool BF16>

@@ -55,6 +55,7 @@ struct NormArgs {
     int ndt;
     long long ns;
     float *out_scale;                   // [T]
+    float len, inv;                     // d and 1 / d (launch_norm sets them)
 };
 hipError_t launch_norm(const NormArgs &a, hipStream_t s);
 
