@@ -13,6 +13,11 @@ namespace moeffn {
 
 namespace {
 
+// All loads so far have landed.  Which of them a later instruction would wait for depends on operands that
+// may be null and on their types, and where the compiler cannot tell it waits for all loads, the
+// next row's among them: it is told here, where all are needed.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+
 // The norm of a row in place, n[c] of whose elements each group of this lane holds.  Where a sum
 // or the squares pass fp32 everything is taken of values 2^-80 as large, eps of 2^-160 of itself
 // (0 below 2^11: beside squares that pass fp32 that is nothing, and of equal values,
@@ -29,31 +34,35 @@ template <bool LAYER, int L, int C, bool WIDE, bool FULL>
 __device__ __forceinline__ void norm_row(float (&v)[C][8], const int (&n)[C], rio::Team<L> &team, const NormArgs &a,
                                          const void *w, const rio::Raw<WIDE> (&wr)[C], const void *b)
 {
-    float m = 0.f, off = 0.f, ss, k = 1.f;
+    float m = 0.f, ss, k = 1.f;
     // s / d, which is exact where fp32 holds it
     auto mean = [&](float s) {
         const float q = s * a.inv;
         return fmaf(fmaf(-q, a.len, s), a.inv, q);
     };
-    auto centred = [&](int c, int j) { return !LAYER ? v[c][j] : (FULL ? n[c] > 0 : j < n[c]) ? v[c][j] - m : 0.f; };
-    auto stats = [&]() {
+    // the row's sum of g(v - m) (RMS: of g(v)) over its own elements; whole groups count or do not
+    auto sum = [&](auto g) {
         float s = 0.f;
-        if constexpr (LAYER) {
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s += v[c][j];               // (past the row's end: 0)
-            m = mean(team.sum(s));
-            s = 0.f;
-        }
-#pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+            float t = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float e = centred(c, j);
-                s = fmaf(e, e, s);
+                const float e = LAYER ? v[c][j] - m : v[c][j];
+                t = g(FULL || !LAYER || j < n[c] ? e : 0.f, t);
             }
-        ss = team.sum(s);
+            s += !FULL || n[c] > 0 ? t : 0.f;
+        }
+        return team.sum(s);
+    };
+    const auto plain = [](float e, float t) { return t + e; };
+    const auto square = [](float e, float t) { return fmaf(e, e, t); };
+    auto stats = [&]() {
+        if constexpr (LAYER) {
+            m = 0.f;
+            m = mean(sum(plain));
+        }
+        ss = sum(square);
     };
     stats();
     if (__any(!(ss < INFINITY))) {
@@ -67,17 +76,13 @@ __device__ __forceinline__ void norm_row(float (&v)[C][8], const int (&n)[C], ri
     if constexpr (LAYER) {
         const bool far = m != 0.f && !(m * m < ss * a.inv);             // (so where both are 0 by underflow)
         if (__any(far)) {
-            float s = 0.f;
+            const float s = sum(plain), off = mean(s), sq = fmaf(-s, off, ss);
+            ss = far ? (sq < 0.f ? 0.f : sq) : ss;
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s += centred(c, j);
-            s = team.sum(s);
-            if (far) {
-                off = mean(s);
-                ss = fmaf(-s, off, ss);
-                if (ss < 0.f) ss = 0.f;
-            }
+                for (int j = 0; j < 8; ++j) v[c][j] = far ? v[c][j] - m - off : v[c][j];
+            m = far ? 0.f : m;
         }
     }
     const float var = ss * a.inv + a.eps * k * k;
@@ -85,7 +90,7 @@ __device__ __forceinline__ void norm_row(float (&v)[C][8], const int (&n)[C], ri
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = LAYER ? (v[c][j] - m - off) * f : v[c][j] * f;
+        for (int j = 0; j < 8; ++j) v[c][j] = LAYER ? (v[c][j] - m) * f : v[c][j] * f;
         if (w) {
             float x[8];
             rio::floats<WIDE>(wr[c], a.wdt, x);
@@ -94,12 +99,15 @@ __device__ __forceinline__ void norm_row(float (&v)[C][8], const int (&n)[C], ri
         }
         if (b) {
             float x[8];
-            rio::floats<WIDE>(rio::load<WIDE, FULL>(b, a.wdt, 8 * (team.lane() + c * team.lanes()), n[c], a.d & 7), a.wdt, x);
+            const rio::Raw<WIDE> br = rio::load<WIDE, FULL>(b, a.wdt, 8 * (team.lane() + c * team.lanes()), n[c], a.d & 7);
+            loads_done();
+            rio::floats<WIDE>(br, a.wdt, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[c][j] += x[j];
         }
+        if (!FULL)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = (FULL ? n[c] > 0 : j < n[c]) ? v[c][j] : 0.f;
+            for (int j = 0; j < 8; ++j) v[c][j] = j < n[c] ? v[c][j] : 0.f;
     }
 }
 
@@ -141,6 +149,7 @@ norm_kernel(NormArgs a)
     for (; base * G < a.T; base += gridDim.x) {
         const long long t = base * G + team.row();
         const bool live = t < a.T;
+        loads_done();
         int m[C];                                   // n of this row (n is the next one's from its loads on)
         float v[C][8];
 #pragma unroll
@@ -198,9 +207,12 @@ norm_kernel(NormArgs a)
         }
         uint32_t most = 0;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+            uint32_t of = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) most = rio::umax(most, codes::magnitude(v[c][j]));
+            for (int j = 0; j < 8; ++j) of = rio::umax(of, codes::magnitude(v[c][j]));
+            most = rio::umax(most, m[c] > 0 ? of : 0);
+        }
         const codes::Row r = codes::row(team.max(most));
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -213,23 +225,27 @@ norm_kernel(NormArgs a)
     }
 }
 
+template <bool LAYER, int L, int C, bool WIDE, bool FULL, bool BARE>
+hipError_t launch_as(const NormArgs &a, const rio::Shape &h, hipStream_t s)
+{
+    static const int waves = rio::held_waves((const void *)norm_kernel<LAYER, L, C, WIDE, FULL, BARE>);
+    hipLaunchKernelGGL((norm_kernel<LAYER, L, C, WIDE, FULL, BARE>), dim3(rio::grid(h, a.T, waves)), dim3(h.threads), 0, s, a);
+    return hipGetLastError();
+}
+
 template <bool LAYER, bool WIDE, bool FULL, bool BARE>
 hipError_t launch(const NormArgs &a, hipStream_t s)
 {
     // two groups a lane: 4096 x 6144 between norms to 8 bits 46 us against 52, 2048 x 8192 30 against 35;
     // 4096 x 4096 28 against 28; with 32-bit operands, whose registers then spill, 71 against 42
     const rio::Shape h = rio::shape(a.d, WIDE || a.T <= 512 ? rio::kGroups : FULL ? 512 : 256);
-    const dim3 g(rio::grid(h, a.T, h.groups == 2 ? 1024 : 2048)), b(h.threads);
     switch (h.lanes) {
-    case 8: hipLaunchKernelGGL((norm_kernel<LAYER, 8, 1, WIDE, FULL, BARE>), g, b, 0, s, a); break;
-    case 16: hipLaunchKernelGGL((norm_kernel<LAYER, 16, 1, WIDE, FULL, BARE>), g, b, 0, s, a); break;
-    case 32: hipLaunchKernelGGL((norm_kernel<LAYER, 32, 1, WIDE, FULL, BARE>), g, b, 0, s, a); break;
-    case 64: hipLaunchKernelGGL((norm_kernel<LAYER, 64, 1, WIDE, FULL, BARE>), g, b, 0, s, a); break;
-    default:
-        if (h.groups == 1) hipLaunchKernelGGL((norm_kernel<LAYER, 0, 1, WIDE, FULL, BARE>), g, b, 0, s, a);
-        else hipLaunchKernelGGL((norm_kernel<LAYER, 0, 2, WIDE, FULL, BARE>), g, b, 0, s, a);
+    case 8: return launch_as<LAYER, 8, 1, WIDE, FULL, BARE>(a, h, s);
+    case 16: return launch_as<LAYER, 16, 1, WIDE, FULL, BARE>(a, h, s);
+    case 32: return launch_as<LAYER, 32, 1, WIDE, FULL, BARE>(a, h, s);
+    case 64: return launch_as<LAYER, 64, 1, WIDE, FULL, BARE>(a, h, s);
     }
-    return hipGetLastError();
+    return h.groups == 1 ? launch_as<LAYER, 0, 1, WIDE, FULL, BARE>(a, h, s) : launch_as<LAYER, 0, 2, WIDE, FULL, BARE>(a, h, s);
 }
 
 template <bool WIDE, bool FULL>

@@ -129,7 +129,7 @@ hipError_t quantize(const QuantizeArgs &a, hipStream_t s)
     }
     // two groups a lane: 14336 x 4096 35 us against 36.5
     const rio::Shape h = rio::shape(a.k, a.T <= 512 ? rio::kGroups : 256);
-    const dim3 g(rio::grid(h, a.T, 1536)), b(h.threads);
+    const dim3 g(rio::grid(h, a.T, 24)), b(h.threads);
     switch (h.lanes) {
     case 8: hipLaunchKernelGGL((quantize_kernel<XDT, 8, 1>), g, b, 0, s, a); break;
     case 16: hipLaunchKernelGGL((quantize_kernel<XDT, 16, 1>), g, b, 0, s, a); break;

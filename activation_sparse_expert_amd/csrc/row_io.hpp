@@ -302,13 +302,23 @@ inline Shape shape(int k, int two)
     return {0, 64 * ((n8 + 64 * groups - 1) / (64 * groups)), groups};
 }
 
-// Workgroups for T rows: no more than the chip holds at a time, about `threads` on each of its 256
-// compute units (rows of part of a wave: 16 workgroups), which then take rows one after
-// another, the next one's loads under way.
-inline unsigned grid(const Shape &h, int T, int threads)
+// Waves of a kernel that a compute unit holds
+inline int held_waves(const void *kernel)
+{
+    int n = 0;
+    return hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 64, 0) == hipSuccess && n > 0 ? n : 16;
+}
+
+// Workgroups for T rows: where one has a row, no more than the chip's 256 compute units hold at a time,
+// `waves` each, which then take rows one after another, the next one's loads under way.  (With
+// twice as many, of which half wait, 8192 x 1411 between blocks took 32 us instead of 28.)
+// Rows of part of a wave: 16 workgroups a unit, which holds 5 to 8 of them (300000 x 64 29 us so, 30.4
+// with those; 100000 x 100 26.4, 22.7 with those).
+inline unsigned grid(const Shape &h, int T, int waves)
 {
     const long long wgs = h.lanes ? ((long long)T + 256 / h.lanes - 1) / (256 / h.lanes) : T;
-    const long long held = 256ll * (h.lanes ? 16 : threads > h.threads ? threads / h.threads : 1);
+    const int unit = h.lanes ? 16 : waves / (h.threads / 64);
+    const long long held = 256ll * (unit > 1 ? unit : 1);
     return (unsigned)(wgs < held ? wgs : held);
 }
 
