@@ -6,10 +6,16 @@
 // residual is exact (p and the product agree to a few units, and max|x| has 11 bits), so
 // a quotient that fp32 holds comes out exactly, ties (n + 1/2) among them; any other
 // quotient is at least 2^-19 of itself away from a tie, far more than its error.  So
-// the codes of 16-bit rows are those of exact arithmetic.  32-bit rows take the same
-// steps in 64 bits (24 + 7 bits).  Both p and max|x| carry the power of two that puts max|x| in
-// [1, 2) (that of 2^-100 for smaller ones): nothing overflows, and what underflows has the
-// code 0.  The quotient is rounded by adding 1.5 2^23, whose last bits then are the code.
+// the codes of 16-bit rows are those of exact arithmetic.  Both p and max|x| carry the power of
+// two that puts max|x| in [1, 2) (that of 2^-100 for smaller ones): nothing overflows, and what
+// underflows has the code 0.  The quotient is rounded by adding 1.5 2^23, whose last bits
+// then are the code.
+//
+// 32-bit numbers: x (127 / max|x|) in 64 bits, with the factor to 2^-50 of itself, is off by at most
+// 2^-43.  It is rounded to a multiple of 2^-38 first: ties are such multiples and come out
+// exactly, and a quotient of 24-bit numbers that is no tie is at least 2^-33 away from one (2^-32
+// of itself, which is 1/2 or more) and stays on its side.  Then it is rounded to an integer.
+// Both roundings are those of additions, of 1.5 2^14 and of 1.5 2^52 less that.
 #pragma once
 #include "device.hpp"
 
@@ -44,21 +50,27 @@ __device__ __forceinline__ Row row(uint32_t most)
     return r;
 }
 
-// A 16-bit x, or an fp32 one whose own last bits are not exact anyway: bits whose last 8 are the code
+// A 16-bit x: bits whose last 8 are the code
 __device__ __forceinline__ uint32_t code(float x, const Row &r)
 {
     const float p = x * r.k, c = p * r.inv;
     return __float_as_uint(fmaf(fmaf(-c, r.a, p), r.inv, c) + 12582912.f);
 }
 
-// An fp32 x
-__device__ __forceinline__ uint32_t code64(float x, const Row &r)
+// 127 / max|x|: two Newton steps take the reciprocal from 23 bits to 46 and to 64 bits' own
+__device__ __forceinline__ double factor64(const Row &r)
 {
-    const double p = (double)x * (double)r.k, a = r.a, i0 = r.inv;
-    const double inv = fma(fma(-i0, a, 1.0), i0, i0);           // 46 bits
-    const double c = p * inv;
-    // (1.5 2^52: the same in 64 bits)
-    return (uint32_t)__builtin_bit_cast(uint64_t, fma(fma(-c, a, p), inv, c) + 6755399441055744.0);
+    const double a = r.a, i0 = r.inv, i1 = fma(fma(-i0, a, 1.0), i0, i0);
+    return (double)r.k * fma(fma(-i1, a, 1.0), i1, i1);
+}
+
+// An fp32 x; f: factor64 of its row
+__device__ __forceinline__ uint32_t code64(float x, double f)
+{
+    constexpr double kGrid = 24576.0, kInt = 6755399441055744.0 - kGrid;
+    double grid = kGrid;
+    asm("" : "+s"(grid));               // (else it takes two registers of each lane, over a whole loop)
+    return (uint32_t)__builtin_bit_cast(uint64_t, fma((double)x, f, grid) + kInt);
 }
 
 // The last bytes of four

@@ -45,12 +45,13 @@ struct OwnCodes {
         __syncthreads();
         for (int i = 0; i < (int)(blockDim.x >> 6); ++i) most = rio::umax(most, slots[i]);
         row = codes::row(most);
+        const double f = XDT == 2 ? codes::factor64(row) : 0.0;
         for (int i = 8 * threadIdx.x; i < pad; i += 8 * blockDim.x) {
             float v[8];
             uint32_t q[8];
             rio::floats<XDT == 2>(rio::load<XDT == 2, true>(raw, XDT, i < k ? i : 0, 8, 0), XDT, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = XDT == 2 ? codes::code64(v[j], row) : codes::code(v[j], row);
+            for (int j = 0; j < 8; ++j) q[j] = XDT == 2 ? codes::code64(v[j], f) : codes::code(v[j], row);
             rio::store_codes<true>((int8_t *)codes, i, 8, 0, q, row.ok && i < k);
         }
         __syncthreads();

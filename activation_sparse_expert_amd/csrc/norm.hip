@@ -214,11 +214,12 @@ norm_kernel(NormArgs a)
             most = rio::umax(most, m[c] > 0 ? of : 0);
         }
         const codes::Row r = codes::row(team.max(most));
+        const double f = codes::factor64(r);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             uint32_t q[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = codes::code(v[c][j], r);
+            for (int j = 0; j < 8; ++j) q[j] = codes::code64(v[c][j], f);
             rio::store_codes<FULL>((int8_t *)a.out + t * a.ns, at[c], m[c], a.d & 7, q, r.ok);
         }
         if (team.lane() == 0 && live) a.out_scale[t] = r.scale;

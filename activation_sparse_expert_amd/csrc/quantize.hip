@@ -46,11 +46,12 @@ quantize_kernel(QuantizeArgs a)
         // the next row of these lanes is on its way while this one is finished
         if ((b + gridDim.x) * G < a.T) load_row(t + (long long)gridDim.x * G);
         const codes::Row r = codes::row(team.max(most));
+        const double f = XDT == 2 ? codes::factor64(r) : 0.0;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             uint32_t q[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = XDT == 2 ? codes::code64(v[c][j], r) : codes::code(v[c][j], r);
+            for (int j = 0; j < 8; ++j) q[j] = XDT == 2 ? codes::code64(v[c][j], f) : codes::code(v[c][j], r);
             rio::store_codes(a.q + t * a.qs, at[c], m[c], a.k & 7, q, r.ok);
         }
         if (team.lane() == 0 && t < a.T) a.scale[t] = r.scale;
@@ -72,12 +73,13 @@ quantize_long_kernel(QuantizeArgs a)
             most = rio::umax(most, rio::most<XDT == 2>(rio::load<XDT == 2>(x, XDT, i, a.k - i, a.k & 7), XDT));
         }
         const codes::Row r = codes::row(team.max(most));
+        const double f = XDT == 2 ? codes::factor64(r) : 0.0;
         for (int i = 8 * threadIdx.x; i < a.k; i += 8 * 1024) {
             float v[8];
             uint32_t q[8];
             rio::floats<XDT == 2>(rio::load<XDT == 2>(x, XDT, i, a.k - i, a.k & 7), XDT, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = XDT == 2 ? codes::code64(v[j], r) : codes::code(v[j], r);
+            for (int j = 0; j < 8; ++j) q[j] = XDT == 2 ? codes::code64(v[j], f) : codes::code(v[j], r);
             rio::store_codes(qr, i, a.k - i, a.k & 7, q, r.ok);
         }
         if (threadIdx.x == 0) a.scale[t] = r.scale;
