@@ -174,7 +174,8 @@ hipError_t launch_one(const le::Args<U> &a, hipStream_t s)
     // keeps 4 blocks and the rings fit; fewer when K is short
     int P = 4;
     const int own = XDT >= 0 ? own_raw_bytes(2 * a.K, XDT) + 128 * blocks : 0;
-    if (8 * per + own <= kLds && (long long)units * P < 2048 && blocks >= 8 * P) P = 8;
+    constexpr int kSlots = XDT >= 0 ? 64 : 0;               // the kernel's static LDS
+    if (8 * per + own + kSlots <= kLds && (long long)units * P < 2048 && blocks >= 8 * P) P = 8;
     // 2 where those are enough, codes only: their sums do not depend on it (1 x 4096 x 28672
     // 20.3 us against 21.4, 16 tokens 21.1 against 22.3)
     if (U == st::kI8 && plenty(2ll * units, per)) P = 2;
