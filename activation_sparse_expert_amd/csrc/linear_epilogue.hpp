@@ -63,7 +63,7 @@ __device__ __forceinline__ void finish(const LinearArgs &p, int t, int n, float 
     st::store_el(p.y, p.ydt, (size_t)t * p.ys + n, v[0]);
 }
 
-// Whether four outputs of a token can be read and written together (finish4)
+// Whether four outputs of a token can be read and written together (finish_cols4, add_store4)
 template <int U>
 bool quads(const Args<U> &p)
 {

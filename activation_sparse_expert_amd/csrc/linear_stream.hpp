@@ -4,7 +4,11 @@
 // workgroup that share the rows add their slices through LDS in a fixed order
 // and apply the epilogue.  Workgroups are small (4 waves), so that several share a
 // compute unit and one streams while another starts or ends.
-// Bound by HBM: 1 x 4096 x 28672 (gated) 38 us, 6.2 TB/s; 16 x 14336 x 4096 24 us, 4.8 TB/s.
+// Bound by HBM, 16-bit weights: 1 x 4096 x 28672 (gated) 38 us, 6.2 TB/s; 16 x 14336 x 4096 24 us,
+// 4.8 TB/s.  8-bit codes, two to a 16-bit unit, are half the bytes: 20 us and 12.7 us; one token that is
+// no codes yet is made some in LDS by each workgroup (OwnCodes).  17 to 32 tokens over a long k are
+// bound by the copies into LDS, two thirds of which are tokens that each wave copies for
+// itself: 32 x 14336 x 4096 17.3 us of codes.
 #pragma once
 #include "linear_epilogue.hpp"
 #include "row_io.hpp"

@@ -1,9 +1,10 @@
 // Norms between two blocks: y = rs r + bs g (.) Npost(o), out = Npre(y).  Bound by HBM: a row
 // is held in registers by the lanes of part of a wave, or by a workgroup, so that each
 // operand is read and written once, and mean and squares are two passes over registers.
-// 131072 x 128, bf16: 14 us, 4.8 TB/s; 4096 x 6144 between two norms to codes: 46 us, 3.8 TB/s
-// (three reductions over a workgroup a row, the next row's loads under way); one row 3.2 us, the
-// launch.
+// 131072 x 128, bf16: 12.7 us, 5.3 TB/s; 4096 x 6144 between two norms to codes: 41.7 us, 4.2 TB/s
+// (three reductions over a workgroup a row, the next row's loads under way); one row 3.0 us, the
+// launch.  Layer norms have more to do a value and are bound by instructions where rows are
+// short of a block: 8192 x 2048 alone 15.4 us, RMS 14.0.
 #include "row_io.hpp"
 #include "rows.hpp"
 
@@ -26,10 +27,10 @@ __device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0F70
 // than the deviation that may be much of what is left of a value, and all of it where values are
 // equal: there e = v - m is summed too, its mean `off` is what m is off by, and the squares about
 // m + off are sum e^2 - off sum e.  (Of equal values e is a few units in the last place, these sums
-// are exact and the norm is 0.)  Only such rows take the third sum: taken by all it cost layer
-// norms of 8192 x 2048 17.0 us instead of 16.5.
+// are exact and the norm is 0.)  Only such rows take the third sum: 8192 x 2048 around 5 takes
+// 18.1 us, around 0 15.4.
 // LAYER: layer norms, whose registers the RMS norms would otherwise hold too (4096 x 6144 between
-// two RMS norms to codes 46 us then, 43 so).
+// two RMS norms to codes: 46 us in one instance with them, 43 apart).
 template <bool LAYER, int L, int C, bool WIDE, bool FULL>
 __device__ __forceinline__ void norm_row(float (&v)[C][8], const int (&n)[C], rio::Team<L> &team, const NormArgs &a,
                                          const void *w, const rio::Raw<WIDE> (&wr)[C], const void *b)
@@ -166,8 +167,8 @@ norm_kernel(NormArgs a)
             for (int c = 0; c < C; ++c) rio::floats<WIDE>(orw[c], a.odt, v[c]);
         }
         // The next row of these lanes is on its way while this one is finished, its block from before
-        // the block's norm where that hides more than the registers cost: 2048 x 8192 between norms to
-        // codes 29.6 us against 32.6, but in one group of 16-bit numbers 8192 x 2048 31.4 against 29.3.
+        // the block's norm where that hides more than the registers cost: 4096 x 6144 between norms to
+        // codes 43.2 us against 44.9, but in one group of 16-bit numbers 131072 x 128 26.7 against 25.7.
         constexpr bool kEarly = C > 1 || WIDE;
         const long long next = t + (long long)gridDim.x * G;
         const bool more = (base + gridDim.x) * G < a.T;
@@ -237,8 +238,11 @@ hipError_t launch_as(const NormArgs &a, const rio::Shape &h, hipStream_t s)
 template <bool LAYER, bool WIDE, bool FULL, bool BARE>
 hipError_t launch(const NormArgs &a, hipStream_t s)
 {
-    // two groups a lane: 4096 x 6144 between norms to 8 bits 46 us against 52, 2048 x 8192 30 against 35;
-    // 4096 x 4096 28 against 28; with 32-bit operands, whose registers then spill, 71 against 42
+    // two groups a lane: 2048 x 8192 between norms to 8 bits 28.7 us against 30.8 in one, 4096 x 3001 28.3
+    // against 40.3, but layer norms of 4096 x 5000 40.7 against 35.5; 4096 x 4096 alike.  With 32-bit
+    // operands two groups need more than the 128 registers that 16 waves leave (8 to 50 go to scratch) and
+    // are taken where one does not hold the row, above 8192: 2048 x 16384 on an fp32 stream 79 us, 5.1 TB/s,
+    // layer norms of bf16 rows with fp32 weights 88 us, 3.0 TB/s, of 2048 x 16383 142 us.
     const rio::Shape h = rio::shape(a.d, WIDE || a.T <= 512 ? rio::kGroups : FULL ? 512 : 256);
     switch (h.lanes) {
     case 8: return launch_as<LAYER, 8, 1, WIDE, FULL, BARE>(a, h, s);

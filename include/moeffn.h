@@ -436,7 +436,8 @@ int moe_linear_plan(int T, int k, int n, int gated, int *tokens, int *rows);
  *   v_tj = sx_t sw_j sum_i xq_ti wq_ji,   y = residual + act(v + bias), or with L->w_gate
  *   y = residual + act(vg + bias_gate) (.) (v + bias)
  * The sums of products of codes are exact (32-bit integers); scales, bias and activation
- * are applied in fp32 as moe_linear_forward's are, with one rounding to ydt.
+ * are applied in fp32 as moe_linear_forward's are, with one rounding to ydt.  (sw_j is applied first:
+ * a sum times it has to stay below 2^128, as it does for scales below 2^97.)
  *   x [T][k] in xdt: MOE_I8 codes (any from -128 to 127) with x_scale [T], or MOE_F16,
  *   MOE_BF16 or MOE_F32 (x_scale NULL), which the call makes codes of by
  *   moe_quantize_rows' rule.  A token whose scale is NaN has a row of NaN.
